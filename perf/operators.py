@@ -115,6 +115,7 @@ def _mx_round(w, v, alpha):
     e = _mx_scale(w, alpha)
     x = _pow2(e).unsqueeze(2)
     t = w.double() / x.double() + v.view_as(w).double()  # next to a border 32 bits would round the wrong way
+    t = torch.where(w.abs().amax(2, keepdim=True) > 0, t, 0.0)  # a block of zeros stays one
     m = t.abs()
     # ties go to the value whose mantissa is even: 0.25 -> 0, 0.75 -> 1, 1.25 -> 1, 1.75 -> 2, 2.5 -> 2, 3.5 -> 4, 5 -> 4
     i = (m > 0.25).byte() + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5.0)
@@ -381,7 +382,7 @@ def exact(case, seed):
         n, k = s["w"].shape
         w, v, alpha = s["w"].double().view(n, -1, BLOCK), s["v"].double().view(n, -1, BLOCK), s["alpha"].double()
         x = p2(floor_log2((w.abs().amax(2) * alpha).clamp(min=2.0**-125)) - 2).unsqueeze(2)
-        t = w / x + v
+        t = torch.where(w.abs().amax(2, keepdim=True) > 0, w / x + v, 0.0)
         if op == "quantise":
             return (e2m1(t) * x).view(n, k), x.squeeze(2)
         inside = t.abs() <= 6
