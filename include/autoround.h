@@ -47,7 +47,7 @@ typedef struct CUstream_st* ar_stream_t; /* same handle as cudaStream_t */
 
 typedef enum {
   AR_OK = 0,
-  AR_ERR_INVALID_ARG = 1, /* null/misaligned pointer, bad size or shape */
+  AR_ERR_INVALID_ARG = 1, /* null/misaligned pointer, bad size or shape; device status: an index out of range */
   AR_ERR_UNSUPPORTED = 2, /* valid request the library does not implement */
   AR_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed */
   AR_ERR_NONFINITE = 4,   /* device status: NaN/Inf seen in an input or gradient */
@@ -477,6 +477,136 @@ AR_API ar_status ar_tune_step_nvfp4(const uint16_t* W, float* V, float* alpha, i
                                     float* loss_per_step, float* dV_out, float* dalpha_out, void* workspace,
                                     size_t workspace_bytes, ar_stream_t stream);
 
+/* MXFP4 fake quantization: a further data type through its tensor-level QDQ
+ * function ([AR] §4 "Why the Tuning Stage Must Take the QDQ Path", point 3, which
+ * names MXFP4).  The pages give no layout; this is the OCP microscaling one: E2M1
+ * values with one power-of-two scale per block of 32 along K, no per-tensor
+ * scale.  Per block b:
+ *   X_b = 2^(floor(log2(alpha_b max_b |W|)) - 2), not below 2^-127
+ *   q = E2M1(W / X_b + V),  W_hat = q X_b      (0 for a block of zeros)
+ * floor, sum and rounding are decided on the exact values (E2M1: nearest, ties to
+ * even, saturating at 6).
+ *   W      bf16 [N][K], K % 32 == 0, 16-byte aligned
+ *   V      fp32 [N][K] offsets, or NULL (0); 16-byte aligned
+ *   alpha  fp32 [N][K/32] clip factors (> 0), or NULL (1)
+ * Outputs, each optional (at least one):
+ *   W_hat   bf16 [N][K] (exact); 16-byte aligned
+ *   codes   uint8 [N][K/2]: two E2M1 codes per byte along K, element k in the low
+ *           nibble when k is even; 16-byte aligned
+ *   scales  uint8 [N][K/32]: E8M0 codes, the exponent of X_b + 127 (0 for a block
+ *           of zeros)
+ * A block with a NaN or Inf (in W or alpha) gets scale code 255 (NaN), codes 0 and
+ * W_hat NaN and raises AR_ERR_NONFINITE in the device status, as a NaN or Inf in V
+ * does.  Errors: AR_ERR_INVALID_ARG / AR_ERR_UNSUPPORTED before any launch. */
+AR_API ar_status ar_qdq_mxfp4(const uint16_t* W, const float* V, const float* alpha, int64_t N, int64_t K,
+                              uint16_t* W_hat, uint8_t* codes, uint8_t* scales, ar_stream_t stream);
+
+/* Its straight-through backward from dW_hat = dL/dW_hat (fp32 [N][K]): both
+ * roundings (the scale's exponent, the codes) count as the identity and the
+ * gradient passes where |W/X + V| <= 6 (m = 1), as in ar_tune_step_nvfp4:
+ *   dV = dW_hat X m,   dalpha_b = (X_b / alpha_b) sum_block dW_hat (q - m W / X)
+ * (dX/dalpha = X / alpha).  0 for a block of zeros; dalpha_b is 0 where X_b is held
+ * at 2^-127.  W, V, alpha as in the forward (V, alpha may be NULL).
+ *   dV     fp32 [N][K], 16-byte aligned, and dalpha fp32 [N][K/32]: at least one
+ * Blocks are summed in a fixed order. */
+AR_API ar_status ar_qdq_mxfp4_backward(const float* dW_hat, const uint16_t* W, const float* V, const float* alpha,
+                                       int64_t N, int64_t K, float* dV, float* dalpha, ar_stream_t stream);
+
+/* Tuning steps of one linear layer on MXFP4: ar_tune_step_nvfp4 with ar_qdq_mxfp4
+ * as its QDQ function and ar_qdq_mxfp4_backward's gradients; alpha fp32 [N][K/32],
+ * K % 32 == 0, N % 8 == 0, M % 8 == 0, no amax.  Other arguments, the in-place
+ * updates and the errors are ar_tune_step_nvfp4's. */
+AR_API size_t ar_tune_step_mxfp4_workspace(int64_t M, int64_t N, int64_t K, int n_steps);
+AR_API ar_status ar_tune_step_mxfp4(const uint16_t* W, float* V, float* alpha, int64_t N, int64_t K, const uint16_t* X,
+                                    int64_t M, const float* Y, const ar_qconfig* cfg, int n_steps,
+                                    float* loss_per_step, float* dV_out, float* dalpha_out, void* workspace,
+                                    size_t workspace_bytes, ar_stream_t stream);
+
+/* Matmul with MXFP4 weights as ar_qdq_mxfp4 exports them, for bf16 activations:
+ *   out[t][n] = sum_k A[t][k] 2^(scales[n][k/32] - 127) E2M1(codes[n][k])
+ *   A       bf16 [T][K], 16-byte aligned
+ *   codes   uint8 [N][K/2], scales uint8 [N][K/32], 16-byte aligned.  Scale codes up
+ *           to 252 (the largest ar_qdq_mxfp4 writes for finite weights) give finite
+ *           weights, 255 makes the whole row NaN
+ *   out     bf16 [T][N] (round to nearest even of fp32 sums), 16-byte aligned
+ * Weights are exact in bf16, so only the fp32 accumulation and the output round.
+ * Small T decodes against the packed weights; larger T runs a tcgen05 GEMM that
+ * dequantizes on the way; at T >= 512 with N % 8 == 0 and a workspace the weights are
+ * expanded once into it and the pair GEMM runs (without a workspace: the
+ * dequantizing GEMM).  Results are deterministic for given sizes.
+ * Needs 1 <= T < 2^31, N >= 1, K % 32 == 0.
+ * workspace: ar_mxfp4_gemm_workspace bytes (device, 256-byte aligned), or NULL. */
+AR_API size_t ar_mxfp4_gemm_workspace(int64_t T, int64_t N, int64_t K);
+AR_API ar_status ar_mxfp4_gemm(const uint16_t* A, int64_t T, const uint8_t* codes, const uint8_t* scales, int64_t N,
+                               int64_t K, uint16_t* out, void* workspace, size_t workspace_bytes, ar_stream_t stream);
+
+/* ---- decoding: a paged 8-bit cache of keys and values ---------------------
+ * The pages name KV-cache quantization (FP8) beside weight quantization without a
+ * layout.  Here a page holds page_size tokens of ONE sequence; per key/value head
+ * it is a [page_size][head_dim] array of E4M3 codes, with one power-of-two scale
+ * (E8M0 code: the exponent + 127) for its keys and one for its values:
+ *   k_pages, v_pages    uint8 [n_pages][n_kv_heads][page_size][head_dim]
+ *   k_scales, v_scales  uint8 [n_pages][n_kv_heads]
+ *   page_table          int32 [S][max_pages]: token j of sequence s is in page
+ *                       page_table[s][j / page_size], place j % page_size.  Entries
+ *                       past a sequence's last token are not read
+ * A batch adds new tokens to S sequences (S <= 4096): rows cu_seqlens[s] ..
+ * cu_seqlens[s+1] - 1 of the token arrays (cu_seqlens int32 [S+1], not falling; a
+ * sequence may have none) are the LAST tokens of sequence s, whose length with them
+ * is seq_lens[s] (int32 [S]).  The same arrays serve ar_kv8_append and then
+ * ar_attention_kv8.  Rows behind cu_seqlens[S] are not touched.
+ * These arrays live on the device and are checked there: bounds that do not fit
+ * (rows outside the T given, lengths beyond max_pages, page numbers outside the
+ * pool) are skipped without touching memory and raise AR_ERR_INVALID_ARG in the
+ * device status (ar_get_device_status). */
+typedef struct {
+  int n_heads;       /* query heads, a multiple of n_kv_heads */
+  int n_kv_heads;
+  int head_dim;      /* 64 or 128 */
+  int page_size;     /* 16, 32, 64 or 128 */
+  int64_t n_pages;   /* pages in the pool; n_pages * n_kv_heads * page_size < 2^31 */
+  int64_t max_pages; /* row length of page_table; max_pages * page_size <= 2^30 */
+} ar_kv8_cfg;
+
+/* Rotates the new tokens' queries and keys by their positions (as the decoder
+ * block above, with rope_base in place of 10000; the angle in fp64), quantizes
+ * keys and values and writes them into their pages, and writes the rotated queries.
+ *   qkv    bf16 [T][(n_heads + 2 n_kv_heads) head_dim]: Q | K | V columns
+ *   q_out  bf16 [T][n_heads head_dim]
+ * Per page and head, over the page's new tokens: e = the smallest exponent with
+ * max |x| <= 448 2^e (within -100..120), at least the page's present exponent when
+ * the page holds older tokens, which are then re-coded as E4M3(code 2^(e_old - e));
+ * new codes are E4M3(x 2^-e) (nearest even) of the fp32 values.  Infinities are
+ * stored as +-448 2^e, NaN as 0, and raise AR_ERR_NONFINITE.
+ * A page that is written belongs to one sequence of the call (full pages may be
+ * shared between sequences).  max_new: an upper bound of a sequence's new tokens
+ * (longer ones are refused on the device); 1 <= rope_base < 1e30. */
+AR_API ar_status ar_kv8_append(const ar_kv8_cfg* cfg, const uint16_t* qkv, int64_t T, const int32_t* cu_seqlens,
+                               const int32_t* seq_lens, const int32_t* page_table, int64_t S, int64_t max_new,
+                               double rope_base, uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_scales,
+                               uint8_t* v_scales, uint16_t* q_out, ar_stream_t stream);
+
+/* Causal softmax attention of the new tokens over their sequences' cache:
+ *   out[t] = sum_j softmax_j(sm_scale q[t] . k_j) v_j, j <= the token's position,
+ * query head h reading key/value head h / (n_heads / n_kv_heads).
+ *   q    bf16 [T][n_heads head_dim] (ar_kv8_append's q_out)
+ *   out  bf16 [T][n_heads head_dim]
+ *   lse  fp32 [T][n_heads], the log-sum-exp of the scaled scores, or NULL
+ * sm_scale 0 means 1/sqrt(head_dim).  A row that sees no key (a sequence shorter
+ * than its new tokens) gets out 0 and lse -inf.  max_new: the longest sequence's
+ * new tokens (it sets the tile height; a longer sequence still comes out right).
+ * The result does not depend on timing; the lengths may change between replays
+ * of a captured call.  Codes 0x7F and 0xFF (NaN) are not written by ar_kv8_append;
+ * places past a sequence's end may hold anything.
+ * workspace: ar_attention_kv8_workspace bytes (device, 256-byte aligned); calls that
+ * overlap on the GPU need one each. */
+AR_API size_t ar_attention_kv8_workspace(const ar_kv8_cfg* cfg, int64_t T, int64_t S, int64_t max_new);
+AR_API ar_status ar_attention_kv8(const ar_kv8_cfg* cfg, const uint16_t* q, int64_t T, const int32_t* cu_seqlens,
+                                  const int32_t* seq_lens, const int32_t* page_table, int64_t S, int64_t max_new,
+                                  float sm_scale, const uint8_t* k_pages, const uint8_t* v_pages,
+                                  const uint8_t* k_scales, const uint8_t* v_scales, uint16_t* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, ar_stream_t stream);
+
 /* Minibatch assembly for block-by-block tuning ([AR] §8 preset table: each
  * iteration works on a batch of 8 -- 4 in the "fast" preset -- of the 128
  * calibration samples; [AR] §3 "Algorithm Flow" steps 3-6 iterate on such
@@ -507,8 +637,9 @@ AR_API ar_status ar_gemm_bf16(const uint16_t* A, int a_mn_major, const uint16_t*
 AR_API ar_status ar_debug_wait_timeout(uint64_t limit_ns, int* gave_up, ar_stream_t stream);
 
 /* Synchronizes `stream`, then returns and clears the sticky device status:
- * AR_OK, AR_ERR_NONFINITE or AR_ERR_TIMEOUT (timeout wins if both are set),
- * or AR_ERR_CUDA if the synchronization itself failed. */
+ * AR_OK, AR_ERR_TIMEOUT, AR_ERR_INVALID_ARG (a page number or sequence bound read
+ * on the device was out of range) or AR_ERR_NONFINITE (the first of these that is
+ * set), or AR_ERR_CUDA if the synchronization itself failed. */
 AR_API ar_status ar_get_device_status(ar_stream_t stream);
 
 /* One line describing the last error of this host thread ("" if none). */

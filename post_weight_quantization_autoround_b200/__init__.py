@@ -26,6 +26,9 @@ __all__ = [
     "ar_tune_step_shard", "DecoderCfg", "DECODER_LAYERS", "ar_decoder_forward_workspace", "ar_decoder_forward",
     "ar_tune_step_decoder_workspace", "ar_tune_step_decoder", "ar_rmsnorm", "ar_attention_forward",
     "ar_attention_backward_workspace", "ar_attention_backward",
+    "ar_qdq_mxfp4", "ar_qdq_mxfp4_backward", "ar_tune_step_mxfp4_workspace", "ar_tune_step_mxfp4",
+    "ar_mxfp4_gemm_workspace", "ar_mxfp4_gemm", "Kv8Cfg", "ar_kv8_append", "ar_attention_kv8_workspace",
+    "ar_attention_kv8",
 ]
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libautoround.so")
@@ -64,6 +67,11 @@ class Grads(ctypes.Structure):
 class DecoderCfg(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int64), ("intermediate", ctypes.c_int64), ("n_heads", ctypes.c_int),
                 ("seq_len", ctypes.c_int64), ("gamma1", ctypes.c_void_p), ("gamma2", ctypes.c_void_p)]
+
+
+class Kv8Cfg(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int64), ("max_pages", ctypes.c_int64)]
 
 
 DECODER_LAYERS = ("q", "k", "v", "o", "gate", "up", "down")
@@ -118,6 +126,18 @@ _SIGNATURES = {
     "ar_tune_step_nvfp4_workspace": (ctypes.c_size_t, [_I64, _I64, _I64, _INT]),
     "ar_tune_step_nvfp4": (_INT, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _P, ctypes.POINTER(QConfig), _INT, _P, _P, _P,
                                   _P, ctypes.c_size_t, _P]),
+    "ar_qdq_mxfp4": (_INT, [_P, _P, _P, _I64, _I64, _P, _P, _P, _P]),
+    "ar_qdq_mxfp4_backward": (_INT, [_P, _P, _P, _P, _I64, _I64, _P, _P, _P]),
+    "ar_tune_step_mxfp4_workspace": (ctypes.c_size_t, [_I64, _I64, _I64, _INT]),
+    "ar_tune_step_mxfp4": (_INT, [_P, _P, _P, _I64, _I64, _P, _I64, _P, ctypes.POINTER(QConfig), _INT, _P, _P, _P, _P,
+                                  ctypes.c_size_t, _P]),
+    "ar_mxfp4_gemm_workspace": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "ar_mxfp4_gemm": (_INT, [_P, _I64, _P, _P, _I64, _I64, _P, _P, ctypes.c_size_t, _P]),
+    "ar_kv8_append": (_INT, [ctypes.POINTER(Kv8Cfg), _P, _I64, _P, _P, _P, _I64, _I64, ctypes.c_double, _P, _P, _P, _P,
+                             _P, _P]),
+    "ar_attention_kv8_workspace": (ctypes.c_size_t, [ctypes.POINTER(Kv8Cfg), _I64, _I64, _I64]),
+    "ar_attention_kv8": (_INT, [ctypes.POINTER(Kv8Cfg), _P, _I64, _P, _P, _P, _I64, _I64, ctypes.c_float, _P, _P, _P, _P,
+                                _P, _P, _P, ctypes.c_size_t, _P]),
 }
 
 
@@ -518,3 +538,135 @@ def ar_attention_backward(qkv, out, dout, lse, S: int, L: int, n_heads: int, dqk
     _check(lib().ar_attention_backward(_ptr(qkv), _ptr(out), _ptr(dout), _ptr(lse), S, L, H, n_heads, _ptr(dqkv),
                                        _ptr(workspace), workspace.numel() * workspace.element_size(),
                                        _stream(stream)))
+
+
+# ---- MXFP4 weights -----------------------------------------------------------
+
+def _typed(t: Optional[torch.Tensor], dtype, shape, name: str, device=None) -> Optional[int]:
+    """``_ptr`` of a tensor of the given type and shape on the current device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ARError(AR_ERR_INVALID_ARG, f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ARError(AR_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current device")
+    return _ptr(t)
+
+
+def ar_qdq_mxfp4(W, V=None, alpha=None, W_hat=None, codes=None, scales=None, stream=None) -> None:
+    """MXFP4 fake quantization of W [N][K] (bf16): V [N][K] fp32 or None, alpha [N][K/32] fp32 or None; outputs
+    W_hat bf16 [N][K], codes uint8 [N][K/2], scales uint8 [N][K/32] (E8M0 codes), each optional."""
+    N, K = W.shape
+    _check(lib().ar_qdq_mxfp4(_typed(W, torch.bfloat16, (N, K), "W"), _typed(V, torch.float32, (N, K), "V"),
+                              _typed(alpha, torch.float32, (N, K // 32), "alpha"), N, K,
+                              _typed(W_hat, torch.bfloat16, (N, K), "W_hat"),
+                              _typed(codes, torch.uint8, (N, K // 2), "codes"),
+                              _typed(scales, torch.uint8, (N, K // 32), "scales"), _stream(stream)))
+
+
+def ar_qdq_mxfp4_backward(dW_hat, W, V, alpha, dV=None, dalpha=None, stream=None) -> None:
+    """Straight-through gradients of ``ar_qdq_mxfp4``: dV fp32 [N][K], dalpha fp32 [N][K/32] from dW_hat fp32 [N][K]."""
+    N, K = W.shape
+    _check(lib().ar_qdq_mxfp4_backward(_typed(dW_hat, torch.float32, (N, K), "dW_hat"),
+                                       _typed(W, torch.bfloat16, (N, K), "W"), _typed(V, torch.float32, (N, K), "V"),
+                                       _typed(alpha, torch.float32, (N, K // 32), "alpha"), N, K,
+                                       _typed(dV, torch.float32, (N, K), "dV"),
+                                       _typed(dalpha, torch.float32, (N, K // 32), "dalpha"), _stream(stream)))
+
+
+def ar_tune_step_mxfp4_workspace(M: int, N: int, K: int, n_steps: int) -> int:
+    n = lib().ar_tune_step_mxfp4_workspace(M, N, K, n_steps)
+    if n == 0:
+        raise ARError(AR_ERR_INVALID_ARG, ar_last_error())
+    return int(n)
+
+
+def ar_tune_step_mxfp4(W, V, alpha, X, Y, cfg: QConfig, n_steps: int, loss_per_step, workspace, dV=None, dalpha=None,
+                       stream=None) -> None:
+    """``n_steps`` SignSGD steps of one linear layer on MXFP4 (V [N][K], alpha [N][K/32] updated in place);
+    loss_per_step: fp32 device [max(n_steps, 1)]; workspace: uint8 device tensor of
+    ``ar_tune_step_mxfp4_workspace`` bytes."""
+    N, K = W.shape
+    M = X.shape[0]
+    _check(lib().ar_tune_step_mxfp4(_typed(W, torch.bfloat16, (N, K), "W"), _typed(V, torch.float32, (N, K), "V"),
+                                    _typed(alpha, torch.float32, (N, K // 32), "alpha"), N, K,
+                                    _typed(X, torch.bfloat16, (M, K), "X"), M, _typed(Y, torch.float32, (M, N), "Y"),
+                                    ctypes.byref(cfg), n_steps,
+                                    _typed(loss_per_step, torch.float32, (max(n_steps, 1),), "loss_per_step"),
+                                    _typed(dV, torch.float32, (N, K), "dV"),
+                                    _typed(dalpha, torch.float32, (N, K // 32), "dalpha"), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def ar_mxfp4_gemm_workspace(T: int, N: int, K: int) -> int:
+    n = lib().ar_mxfp4_gemm_workspace(T, N, K)
+    if n == 0:
+        raise ARError(AR_ERR_INVALID_ARG, ar_last_error())
+    return int(n)
+
+
+def ar_mxfp4_gemm(A, codes, scales, out, workspace=None, stream=None) -> None:
+    """out [T][N] bf16 = A [T][K] bf16 times the MXFP4 weights (codes uint8 [N][K/2], scales uint8 [N][K/32] as
+    ``ar_qdq_mxfp4`` writes them); workspace: ``ar_mxfp4_gemm_workspace`` bytes, or None."""
+    T, K = A.shape
+    N = codes.shape[0]
+    _check(lib().ar_mxfp4_gemm(_typed(A, torch.bfloat16, (T, K), "A"), T, _typed(codes, torch.uint8, (N, K // 2), "codes"),
+                               _typed(scales, torch.uint8, (N, K // 32), "scales"), N, K,
+                               _typed(out, torch.bfloat16, (T, N), "out"), _ptr(workspace),
+                               0 if workspace is None else workspace.numel() * workspace.element_size(),
+                               _stream(stream)))
+
+
+# ---- the paged 8-bit cache ----------------------------------------------------
+
+def _kv8(cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, n_heads: int):
+    """The cache's description and the pointers that both calls take."""
+    n_pages, n_kv, page, d = k_pages.shape
+    S, max_pages = page_table.shape
+    cfg = Kv8Cfg(n_heads, n_kv, d, page, n_pages, max_pages)
+    index = (_typed(cu_seqlens, torch.int32, (S + 1,), "cu_seqlens"), _typed(seq_lens, torch.int32, (S,), "seq_lens"),
+             _typed(page_table, torch.int32, (S, max_pages), "page_table"))
+    shape = (n_pages, n_kv, page, d)
+    cache = (_typed(k_pages, torch.uint8, shape, "k_pages"), _typed(v_pages, torch.uint8, shape, "v_pages"),
+             _typed(k_scales, torch.uint8, shape[:2], "k_scales"), _typed(v_scales, torch.uint8, shape[:2], "v_scales"))
+    return cfg, index, cache, S
+
+
+def ar_kv8_append(qkv, cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, q_out, max_new: int,
+                  rope_base: float = 10000.0, stream=None) -> None:
+    """Rotate, quantize and write the new tokens' keys and values into their pages; q_out gets the rotated queries.
+
+    qkv bf16 [T][(n_heads + 2 n_kv) d]; k_pages, v_pages uint8 [n_pages][n_kv][page][d]; k_scales, v_scales uint8
+    [n_pages][n_kv]; page_table int32 [S][max_pages]; cu_seqlens int32 [S+1]; seq_lens int32 [S], the new tokens
+    included; q_out bf16 [T][n_heads d]; max_new an upper bound of a sequence's new tokens.
+    """
+    T, width = qkv.shape
+    n_kv, d = k_pages.shape[1], k_pages.shape[3]
+    n_heads = width // d - 2 * n_kv
+    cfg, index, cache, S = _kv8(cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, n_heads)
+    _check(lib().ar_kv8_append(ctypes.byref(cfg), _typed(qkv, torch.bfloat16, (T, (n_heads + 2 * n_kv) * d), "qkv"), T,
+                               *index, S, max_new, rope_base, *cache,
+                               _typed(q_out, torch.bfloat16, (T, n_heads * d), "q_out"), _stream(stream)))
+
+
+def ar_attention_kv8_workspace(T: int, S: int, max_new: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                               page_size: int, n_pages: int, max_pages: int) -> int:
+    cfg = Kv8Cfg(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages)
+    n = lib().ar_attention_kv8_workspace(ctypes.byref(cfg), T, S, max_new)
+    if n == 0:
+        raise ARError(AR_ERR_INVALID_ARG, ar_last_error())
+    return int(n)
+
+
+def ar_attention_kv8(q, cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, out, max_new: int,
+                     workspace, lse=None, sm_scale: float = 0.0, stream=None) -> None:
+    """Causal attention of the new tokens (q, out bf16 [T][n_heads d]) over their sequences' cached keys and values;
+    lse fp32 [T][n_heads] or None; sm_scale 0 is 1/sqrt(d); workspace: ``ar_attention_kv8_workspace`` bytes."""
+    T, width = q.shape
+    n_heads = width // k_pages.shape[3]
+    cfg, index, cache, S = _kv8(cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, n_heads)
+    shape = (T, n_heads * k_pages.shape[3])
+    _check(lib().ar_attention_kv8(ctypes.byref(cfg), _typed(q, torch.bfloat16, shape, "q"), T, *index, S, max_new,
+                                  sm_scale, *cache, _typed(out, torch.bfloat16, shape, "out"),
+                                  _typed(lse, torch.float32, (T, n_heads), "lse"), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream(stream)))

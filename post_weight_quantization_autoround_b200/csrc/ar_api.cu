@@ -1069,6 +1069,261 @@ ar_status ar_tune_step_nvfp4(const uint16_t* W, float* V, float* alpha, int64_t 
   return end_call();
 }
 
+static ar_status check_mxfp4(int64_t N, int64_t K) {
+  if (N <= 0 || K <= 0) return fail(AR_ERR_INVALID_ARG, "N, K must be positive");
+  if (K % 32 != 0) return fail(AR_ERR_INVALID_ARG, "K=%lld is not a multiple of the 32-value block", (long long)K);
+  if (N > (int64_t(1) << 42) / K) return fail(AR_ERR_UNSUPPORTED, "N*K exceeds 2^42");
+  return AR_OK;
+}
+
+ar_status ar_qdq_mxfp4(const uint16_t* W, const float* V, const float* alpha, int64_t N, int64_t K, uint16_t* W_hat,
+                       uint8_t* codes, uint8_t* scales, ar_stream_t stream) {
+  begin_call();
+  ar_status st = check_mxfp4(N, K);
+  if (st != AR_OK) return st;
+  if (!W) return fail(AR_ERR_INVALID_ARG, "NULL input pointer");
+  if (!W_hat && !codes && !scales) return fail(AR_ERR_INVALID_ARG, "no output requested");
+  const void* a16[] = {W, V, W_hat, codes};
+  for (const void* p : a16)
+    if (p && !aligned16(p)) return fail(AR_ERR_INVALID_ARG, "W, V, W_hat and codes must be 16-byte aligned");
+  if (alpha && !aligned4(alpha)) return fail(AR_ERR_INVALID_ARG, "alpha must be 4-byte aligned");
+  cudaError_t e = launch_qdq_mxfp4(W, V, alpha, N * K, W_hat, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qdq_mxfp4 launch");
+  return end_call();
+}
+
+ar_status ar_qdq_mxfp4_backward(const float* dW_hat, const uint16_t* W, const float* V, const float* alpha, int64_t N,
+                                int64_t K, float* dV, float* dalpha, ar_stream_t stream) {
+  begin_call();
+  ar_status st = check_mxfp4(N, K);
+  if (st != AR_OK) return st;
+  if (!dW_hat || !W) return fail(AR_ERR_INVALID_ARG, "NULL input pointer");
+  if (!dV && !dalpha) return fail(AR_ERR_INVALID_ARG, "no output requested");
+  const void* a16[] = {dW_hat, W, V, dV};
+  for (const void* p : a16)
+    if (p && !aligned16(p)) return fail(AR_ERR_INVALID_ARG, "dW_hat, W, V and dV must be 16-byte aligned");
+  if ((alpha && !aligned4(alpha)) || (dalpha && !aligned4(dalpha)))
+    return fail(AR_ERR_INVALID_ARG, "alpha and dalpha must be 4-byte aligned");
+  cudaError_t e = launch_bwd_mxfp4(dW_hat, W, V, alpha, N * K, dV, dalpha, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "bwd_mxfp4 launch");
+  return end_call();
+}
+
+static ar_status check_mxfp4_step(int64_t M, int64_t N, int64_t K, int n_steps) {
+  ar_status st = check_mxfp4(N, K);
+  if (st != AR_OK) return st;
+  if (M <= 0) return fail(AR_ERR_INVALID_ARG, "sizes must be positive");
+  if (N % 8 != 0 || M % 8 != 0) return fail(AR_ERR_INVALID_ARG, "N and M must be multiples of 8");
+  if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return fail(AR_ERR_UNSUPPORTED, "dimension exceeds 2^31-1");
+  if (n_steps < 0) return fail(AR_ERR_INVALID_ARG, "n_steps must be >= 0");
+  return AR_OK;
+}
+
+size_t ar_tune_step_mxfp4_workspace(int64_t M, int64_t N, int64_t K, int n_steps) {
+  begin_call();
+  if (check_mxfp4_step(M, N, K, n_steps) != AR_OK) return 0;
+  return nvfp4_ws(M, N, K, n_steps).total;  // the same buffers as an NVFP4 step
+}
+
+ar_status ar_tune_step_mxfp4(const uint16_t* W, float* V, float* alpha, int64_t N, int64_t K, const uint16_t* X,
+                             int64_t M, const float* Y, const ar_qconfig* cfg, int n_steps, float* loss_per_step,
+                             float* dV_out, float* dalpha_out, void* workspace, size_t workspace_bytes,
+                             ar_stream_t stream) {
+  begin_call();
+  ar_status st = check_cfg(cfg);
+  if (st != AR_OK) return st;
+  st = check_mxfp4_step(M, N, K, n_steps);
+  if (st != AR_OK) return st;
+  if (!W || !V || !alpha || !X || !Y || !loss_per_step) return fail(AR_ERR_INVALID_ARG, "NULL pointer");
+  const void* a16[] = {W, V, alpha, X, Y, dV_out};
+  for (const void* p : a16)
+    if (p && !aligned16(p)) return fail(AR_ERR_INVALID_ARG, "W, V, alpha, X, Y and dV_out must be 16-byte aligned");
+  if (!aligned4(loss_per_step) || (dalpha_out && !aligned4(dalpha_out)))
+    return fail(AR_ERR_INVALID_ARG, "loss_per_step and dalpha_out must be 4-byte aligned");
+  const Nvfp4Ws w = nvfp4_ws(M, N, K, n_steps);
+  if (!workspace || workspace_bytes < w.total)
+    return fail(AR_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", w.total, workspace_bytes);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(AR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint16_t* W_hat = reinterpret_cast<uint16_t*>(ws + w.what);
+  uint16_t* G = reinterpret_cast<uint16_t*>(ws + w.g);
+  float* dW = reinterpret_cast<float*>(ws + w.dw);
+  double* partial = reinterpret_cast<double*>(ws + w.partial);
+  const int Mi = static_cast<int>(M), Ni = static_cast<int>(N), Ki = static_cast<int>(K);
+  const float gscale = static_cast<float>(2.0 / (static_cast<double>(M) * static_cast<double>(N)));
+  const int steps = n_steps > 0 ? n_steps : 1;
+  cudaError_t e;
+  for (int step = 0; step < steps; ++step) {
+    e = launch_qdq_mxfp4(W, V, alpha, N * K, W_hat, nullptr, nullptr, s);
+    if (e != cudaSuccess) return cuda_fail(e, "qdq_mxfp4 launch");
+    e = launch_gemm_resid(X, W_hat, Y, G, gscale, partial + static_cast<size_t>(step) * w.partials_per_step, Mi, Ni,
+                          Ki, s);
+    if (e != cudaSuccess) return cuda_fail(e, "forward GEMM launch");
+    if (n_steps == 0) break;
+    // dL/dW_hat [N][K] = G^T X: both operands as stored, MN-major, reduced over the M tokens
+    e = launch_gemm_plain(G, true, X, true, dW, Ni, Ki, Mi, s);
+    if (e != cudaSuccess) return cuda_fail(e, "weight-gradient GEMM launch");
+    const bool last = step == steps - 1;
+    e = launch_fold_mxfp4(dW, W, V, alpha, N * K, cfg->lr, cfg->v_min, cfg->v_max, cfg->clip_min, cfg->clip_max,
+                          last ? dV_out : nullptr, last ? dalpha_out : nullptr, s);
+    if (e != cudaSuccess) return cuda_fail(e, "fold_mxfp4 launch");
+  }
+  e = launch_loss_reduce(partial, w.partials_per_step, steps, 1.0 / (static_cast<double>(M) * static_cast<double>(N)),
+                         loss_per_step, s);
+  if (e != cudaSuccess) return cuda_fail(e, "loss reduction launch");
+  return end_call();
+}
+
+// From this many tokens the product expands the weights to bf16 once (the caller's workspace) and runs
+// the pair GEMM: the dequantizing GEMM would expand them again for every 128 tokens.
+static constexpr int64_t kMxExpandTokens = 512;
+
+static bool mxfp4_expands(int64_t T, int64_t N) { return T >= kMxExpandTokens && N % 8 == 0; }
+
+size_t ar_mxfp4_gemm_workspace(int64_t T, int64_t N, int64_t K) {
+  begin_call();
+  if (check_mxfp4(N, K) != AR_OK) return 0;
+  if (T < 1 || T > INT32_MAX || N > INT32_MAX || K > INT32_MAX) {
+    fail(AR_ERR_INVALID_ARG, "T, N, K must be in 1..2^31-1");
+    return 0;
+  }
+  return mxfp4_expands(T, N) ? align_up(static_cast<size_t>(N * K) * 2, 256) : 256;
+}
+
+ar_status ar_mxfp4_gemm(const uint16_t* A, int64_t T, const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t K,
+                        uint16_t* out, void* workspace, size_t workspace_bytes, ar_stream_t stream) {
+  begin_call();
+  ar_status st = check_mxfp4(N, K);
+  if (st != AR_OK) return st;
+  if (T < 1) return fail(AR_ERR_INVALID_ARG, "T must be positive");
+  if (N > INT32_MAX || K > INT32_MAX || T > INT32_MAX) return fail(AR_ERR_UNSUPPORTED, "dimension exceeds 2^31-1");
+  const void* ptrs[] = {A, codes, scales, out};
+  for (const void* p : ptrs) {
+    if (!p) return fail(AR_ERR_INVALID_ARG, "NULL pointer");
+    if (!aligned16(p)) return fail(AR_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int Ti = static_cast<int>(T), Ni = static_cast<int>(N), Ki = static_cast<int>(K);
+  cudaError_t e;
+  if (workspace && mxfp4_expands(T, N)) {
+    const size_t need = static_cast<size_t>(N * K) * 2;
+    if (workspace_bytes < need) return fail(AR_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(AR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    uint16_t* W = static_cast<uint16_t*>(workspace);
+    e = launch_expand_mxfp4(codes, scales, N * K, W, s);
+    if (e != cudaSuccess) return cuda_fail(e, "expand_mxfp4 launch");
+    e = launch_gemm_store_bf16(A, W, out, Ti, Ni, Ki, s);
+  } else {
+    e = launch_mxfp4_tc(A, Ti, codes, scales, Ni, Ki, out, s);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "mxfp4 gemm launch");
+  return end_call();
+}
+
+static ar_status kv8_args(const ar_kv8_cfg* cfg, int64_t T, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                          const int32_t* page_table, int64_t S, int64_t max_new, Kv8Args* a) {
+  if (!cfg) return fail(AR_ERR_INVALID_ARG, "cfg is NULL");
+  if (cfg->n_heads <= 0 || cfg->n_kv_heads <= 0 || cfg->n_heads % cfg->n_kv_heads != 0)
+    return fail(AR_ERR_INVALID_ARG, "n_heads must be a positive multiple of n_kv_heads");
+  if (cfg->n_heads > 65536) return fail(AR_ERR_UNSUPPORTED, "n_heads exceeds 65536");
+  if (cfg->head_dim != 64 && cfg->head_dim != 128) return fail(AR_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (cfg->page_size != 16 && cfg->page_size != 32 && cfg->page_size != 64 && cfg->page_size != 128)
+    return fail(AR_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+  if (cfg->n_pages <= 0 || cfg->max_pages <= 0) return fail(AR_ERR_INVALID_ARG, "n_pages and max_pages must be positive");
+  if (cfg->n_pages > INT32_MAX / (static_cast<int64_t>(cfg->n_kv_heads) * cfg->page_size))
+    return fail(AR_ERR_UNSUPPORTED, "n_pages * n_kv_heads * page_size exceeds 2^31-1");
+  if (cfg->max_pages > (1 << 30) / cfg->page_size) return fail(AR_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^30");
+  if (T < 1 || S < 1 || max_new < 1) return fail(AR_ERR_INVALID_ARG, "T, S, max_new must be positive");
+  if (S > kKv8MaxSeqs) return fail(AR_ERR_UNSUPPORTED, "more than %d sequences", kKv8MaxSeqs);
+  if (T > INT32_MAX / cfg->n_heads) return fail(AR_ERR_UNSUPPORTED, "T * n_heads exceeds 2^31-1");
+  if (max_new > T) return fail(AR_ERR_INVALID_ARG, "max_new=%lld exceeds T=%lld", (long long)max_new, (long long)T);
+  *a = Kv8Args{};
+  a->cu = cu_seqlens;
+  a->lens = seq_lens;
+  a->table = page_table;
+  a->T = T;
+  a->S = static_cast<int>(S);
+  a->n_heads = cfg->n_heads;
+  a->n_kv = cfg->n_kv_heads;
+  a->head_dim = cfg->head_dim;
+  a->page = cfg->page_size;
+  a->max_pages = static_cast<int>(cfg->max_pages);
+  a->max_new = static_cast<int>(max_new);
+  a->n_pages = cfg->n_pages;
+  return AR_OK;
+}
+
+static ar_status check_kv8_pointers(const Kv8Args& a, const void* x, const void* y, const void* k, const void* v,
+                                    const void* ks, const void* vs) {
+  const void* p16[] = {x, y, k, v};
+  for (const void* p : p16)
+    if (!p || !aligned16(p)) return fail(AR_ERR_INVALID_ARG, "queries, outputs and pages must be 16-byte aligned device pointers");
+  const void* p4[] = {a.cu, a.lens, a.table};
+  for (const void* p : p4)
+    if (!p || !aligned4(p)) return fail(AR_ERR_INVALID_ARG, "cu_seqlens, seq_lens and page_table must be 4-byte aligned device pointers");
+  if (!ks || !vs) return fail(AR_ERR_INVALID_ARG, "NULL scales");
+  return AR_OK;
+}
+
+ar_status ar_kv8_append(const ar_kv8_cfg* cfg, const uint16_t* qkv, int64_t T, const int32_t* cu_seqlens,
+                        const int32_t* seq_lens, const int32_t* page_table, int64_t S, int64_t max_new,
+                        double rope_base, uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_scales, uint8_t* v_scales,
+                        uint16_t* q_out, ar_stream_t stream) {
+  begin_call();
+  Kv8Args a;
+  ar_status st = kv8_args(cfg, T, cu_seqlens, seq_lens, page_table, S, max_new, &a);
+  if (st != AR_OK) return st;
+  st = check_kv8_pointers(a, qkv, q_out, k_pages, v_pages, k_scales, v_scales);
+  if (st != AR_OK) return st;
+  if (!(rope_base >= 1.0) || !(rope_base < 1e30)) return fail(AR_ERR_INVALID_ARG, "rope_base must be at least 1 and finite");
+  cudaError_t e = launch_kv8_append(a, qkv, rope_base, k_pages, v_pages, k_scales, v_scales, q_out,
+                                    reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv8 append launch");
+  return end_call();
+}
+
+// units of 128 keys that a call can have at most must fit 31 bits
+static ar_status check_kv8_units(const Kv8Args& a) {
+  const double tiles = static_cast<double>(a.T) * (a.n_heads / a.n_kv) / 8.0 + a.S;
+  if (tiles * a.n_kv * (static_cast<double>(a.max_pages) * a.page / 128.0 + 1.0) >= 2147483648.0)
+    return fail(AR_ERR_UNSUPPORTED, "too many row tiles times keys for one call: split the batch");
+  return AR_OK;
+}
+
+size_t ar_attention_kv8_workspace(const ar_kv8_cfg* cfg, int64_t T, int64_t S, int64_t max_new) {
+  begin_call();
+  Kv8Args a;
+  if (kv8_args(cfg, T, nullptr, nullptr, nullptr, S, max_new, &a) != AR_OK) return 0;
+  return align_up(attn_kv8_workspace(a), 256);
+}
+
+ar_status ar_attention_kv8(const ar_kv8_cfg* cfg, const uint16_t* q, int64_t T, const int32_t* cu_seqlens,
+                           const int32_t* seq_lens, const int32_t* page_table, int64_t S, int64_t max_new,
+                           float sm_scale, const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_scales,
+                           const uint8_t* v_scales, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                           ar_stream_t stream) {
+  begin_call();
+  Kv8Args a;
+  ar_status st = kv8_args(cfg, T, cu_seqlens, seq_lens, page_table, S, max_new, &a);
+  if (st != AR_OK) return st;
+  st = check_kv8_pointers(a, q, out, k_pages, v_pages, k_scales, v_scales);
+  if (st != AR_OK) return st;
+  st = check_kv8_units(a);
+  if (st != AR_OK) return st;
+  if (lse && !aligned4(lse)) return fail(AR_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  if (!(sm_scale >= 0.0f) || !(sm_scale < 1e30f)) return fail(AR_ERR_INVALID_ARG, "sm_scale must be finite and >= 0 (0: 1/sqrt(head_dim))");
+  if (sm_scale == 0.0f) sm_scale = 1.0f / sqrtf(static_cast<float>(a.head_dim));
+  const size_t need = attn_kv8_workspace(a);
+  if (!workspace || workspace_bytes < need)
+    return fail(AR_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(AR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  cudaError_t e = launch_attn_kv8(a, q, sm_scale, k_pages, v_pages, k_scales, v_scales, out, lse, workspace,
+                                  reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv8 attention launch");
+  return end_call();
+}
+
 ar_status ar_gemm_bf16(const uint16_t* A, int a_mn_major, const uint16_t* B, int b_mn_major, float* D, int64_t M,
                        int64_t N, int64_t K, ar_stream_t stream) {
   begin_call();
@@ -1098,6 +1353,8 @@ ar_status ar_get_device_status(ar_stream_t stream) {
   cudaError_t e = read_and_clear_status(&v, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(AR_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   if (v & kStatusTimeout) return fail(AR_ERR_TIMEOUT, "a pipeline wait timed out on the device");
+  if (v & kStatusBadIndex)
+    return fail(AR_ERR_INVALID_ARG, "a page number or a sequence bound read on the device was out of range");
   if (v & kStatusNonFinite) return fail(AR_ERR_NONFINITE, "non-finite value seen on the device");
   return AR_OK;
 }

@@ -1,0 +1,688 @@
+// Softmax attention of a batch's new tokens over a paged 8-bit cache (E4M3 codes with a
+// power-of-two scale per page and head, as kv8_append_kernel writes them).
+//
+//   z_j = sm_scale q . k_j,  out = sum_j softmax(z)_j v_j  over the keys j <= position
+//
+// One token a sequence reads its whole cache for a handful of rows, so the kernel is built
+// to stream: bytes of codes per second are the bound, and everything else is kept small.
+//
+//  * Rows are (new token, head of the group) pairs that share a key/value head: R = 8 NT of
+//    them form the columns of the products, S^T = K Q^T and O^T = V^T P^T
+//    (mma.sync m16n8k16, f16 in, fp32 sums): with the cache as the left operand 8 rows fill
+//    an instruction, where the usual order would need 16.
+//  * E4M3 is a subset of f16: one conversion instruction turns two codes into an operand
+//    register, with no scale applied.  Queries become f16 after a power-of-two
+//    normalisation per row (largest value in [2^13, 2^14)): what f16 loses is below 2^-38 of
+//    the row's largest value.  The scales are exponents and go into the softmax: with
+//    u = z log2(e) + e_v, P' = 2^(u - max u) carries the value scale and lies in [0, 1]
+//    whatever the scales, O = sum P' v', and the row sum adds P' 2^-e_v.  P' is f16 (2^-12
+//    relative, finer than the bf16 output), maximum, sum and O are fp32.
+//  * S^T leaves the tensor core with tokens along lanes' rows; movmatrix transposes the
+//    8 x 8 blocks into the B operand of O^T.  V^T comes from ldmatrix.trans on byte pairs:
+//    one byte permute separates even and odd dimensions.
+//  * Each of a block's 8 warps streams its own 16-token tiles (2 KB of keys and of values
+//    at d = 128; TMA boxes with the hardware swizzle, so neither read conflicts)
+//    through a private ring; nothing but the end of an item synchronises the block.  Two
+//    blocks share an SM up to 8 rows, so that one streams while the other joins.
+//  * The work is the list of (sequence, row tile, head, 128 tokens) units.  Every block takes
+//    an equal run of it, found from the lengths on the device (the host does not know them,
+//    and a captured graph keeps working as they grow).  A row tile split between blocks is
+//    joined by a second kernel from unnormalised sums in the workspace, in block order: no
+//    atomics, the same result every time.
+#include <cuda_fp8.h>
+
+#include "ar_internal.h"
+
+namespace ar {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 16;               // tokens of a warp's step
+constexpr int kUnit = kWarps * kTile;   // tokens of a work unit
+constexpr int kChunk = 32;              // steps whose pages and scales the lanes hold
+
+template <int D, int NT>
+struct AttnCfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kBlocksPerSm = NT == 1 ? 2 : 1;
+  static constexpr int kStages = NT == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 4 : 6);
+  static constexpr int kTileBytes = kTile * D;        // of keys, and of values
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kJoinDims = 32;                // dimensions joined per round
+  static constexpr int kJoinStride = kJoinDims + 4;   // floats
+  static constexpr int kJoinBytes = kWarps * kRows * kJoinStride * 4;
+  static constexpr int kSlotFloats = kRows * (D + 2); // a partial result: sums, then maximum and row sum per row
+};
+
+struct AttnCtl {
+  uint64_t full[kWarps][8];
+  float m[kWarps][32], l[kWarps][32];  // per warp and row
+  int abort_flag;
+};
+
+struct AttnParams {
+  Kv8Args a;
+  const uint16_t* q;
+  const uint8_t* ks;
+  const uint8_t* vs;
+  uint16_t* out;
+  float* lse;
+  float* slots;  // [blocks][2][kSlotFloats]
+  int4* desc;    // [blocks]: {sequence, row tile, head, last block} of the item whose first part is the block's, or x = -1
+  float scale_log2;
+};
+
+// a sequence's bounds, checked against the arrays
+struct Seq {
+  int first, n_new, len;  // first new row, new tokens, tokens
+};
+
+__device__ __forceinline__ Seq load_seq(const Kv8Args& a, int s) {
+  const int64_t c0 = a.cu[s], rows = a.cu[s + 1] - c0;
+  const int64_t len = a.lens[s];
+  Seq q;
+  const bool ok = rows >= 0 && c0 >= 0 && c0 + rows <= a.T && len >= 0 && len <= static_cast<int64_t>(a.max_pages) * a.page;
+  if (!ok) raise_status(kStatusBadIndex);
+  q.first = ok ? static_cast<int>(c0) : 0;
+  q.n_new = ok ? static_cast<int>(rows) : 0;
+  q.len = ok ? static_cast<int>(len) : 0;
+  return q;
+}
+
+// keys that the row tile's last row sees
+__device__ __forceinline__ int tile_keys(const Seq& q, int rt, int rows, int group) {
+  const int last = min(q.n_new - 1, (rt * rows + rows - 1) / group);
+  return max(0, q.len - q.n_new + last + 1);
+}
+
+__device__ __forceinline__ int units_of(int keys) { return keys <= kUnit ? 1 : (keys + kUnit - 1) / kUnit; }
+
+__device__ __forceinline__ int row_tiles(const Seq& q, int rows, int group) {
+  return (q.n_new * group + rows - 1) / rows;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 16-byte chunk of a tile's row under the copy's swizzle (128-byte rows: chunk ^ row % 8;
+// 64-byte rows: chunk ^ (row / 2) % 4)
+template <int D>
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+  return static_cast<uint32_t>(row * D + ((D == 128 ? (chunk ^ (row & 7)) : (chunk ^ ((row >> 1) & 3))) << 4));
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, AttnCfg<D, NT>::kBlocksPerSm)
+    attn_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
+  using Cfg = AttnCfg<D, NT>;
+  constexpr int kRows = Cfg::kRows;
+  constexpr int kKs = D / 16;      // k-steps of S^T
+  constexpr int kMt = D / 16;      // 16-dimension tiles of O^T
+  constexpr int kQr = D / 64;      // 16-byte loads of a K row per lane
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* join = reinterpret_cast<float*>(smem + Cfg::kRingBytes);
+  AttnCtl* ctl = reinterpret_cast<AttnCtl*>(smem + Cfg::kRingBytes + Cfg::kJoinBytes);
+  uint32_t* prefix = reinterpret_cast<uint32_t*>(ctl + 1);  // [S + 1] units before each sequence
+  const Kv8Args& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int group = a.n_heads / a.n_kv;
+  uint8_t* ring = smem + warp * Cfg::kStages * Cfg::kStageBytes;
+
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kWarps; ++w)
+      for (int s = 0; s < Cfg::kStages; ++s) mbar_init(&ctl->full[w][s], 1);
+    ctl->abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  // units of every sequence, a warp each
+  for (int s = warp; s < a.S; s += kWarps) {
+    const Seq q = load_seq(a, s);
+    const int nrt = row_tiles(q, kRows, group);
+    uint32_t u = 0;
+    for (int rt = lane; rt < nrt; rt += 32) u += units_of(tile_keys(q, rt, kRows, group));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+    if (lane == 0) prefix[s + 1] = u * a.n_kv;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t run = 0;
+    for (int s0 = 0; s0 < a.S; s0 += 32) {
+      uint32_t v = s0 + lane < a.S ? prefix[s0 + lane + 1] : 0u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += t;
+      }
+      if (s0 + lane < a.S) prefix[s0 + lane + 1] = run + v;
+      run += __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    if (lane == 0) prefix[0] = 0u;
+  }
+  __syncthreads();
+  const uint32_t total = prefix[a.S];
+  const uint32_t quota = (total + gridDim.x - 1) / gridDim.x;
+  const uint32_t u_begin = min(total, blockIdx.x * quota), u_end = min(total, u_begin + quota);
+  if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (u_begin >= u_end) return;
+
+  // where the run starts: sequence, row tile, head, unit
+  int s;
+  {
+    int lo = 0, hi = a.S - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (prefix[mid + 1] > u_begin) hi = mid;
+      else lo = mid + 1;
+    }
+    s = lo;
+  }
+  Seq seq = load_seq(a, s);
+  int rt = 0, head, item_units;
+  uint32_t at = u_begin, item0 = prefix[s];  // item0: first unit of the current row tile's heads
+  for (;; ++rt) {
+    item_units = units_of(tile_keys(seq, rt, kRows, group));
+    const uint32_t next = item0 + static_cast<uint32_t>(item_units) * a.n_kv;
+    if (next > at) break;
+    item0 = next;
+  }
+  head = static_cast<int>((at - item0) / item_units);
+
+  uint32_t stage = 0, phase = 0;
+  bool alive = true;
+
+  while (at < u_end) {
+    const uint32_t first_unit = item0 + static_cast<uint32_t>(head) * item_units;
+    const int t0 = static_cast<int>(at - first_unit);                                  // units of the item done before
+    const int t1 = static_cast<int>(min(u_end - first_unit, static_cast<uint32_t>(item_units)));  // and after this segment
+    const int keys = tile_keys(seq, rt, kRows, group);
+    const int start = seq.len - seq.n_new;
+    const int row0 = rt * kRows;
+    const int n_rows = seq.n_new * group;
+
+    // ---- queries: B operand registers, normalised; a row's factor to log2 units
+    uint32_t qf[NT][kKs][2];
+    float fac[NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g;
+      uint32_t raw[D / 8];  // this lane's D / 4 values (dimensions D / 4 c ..), bf16 pairs
+      if (r < n_rows) {
+        const int tok = r / group, qh = head * group + (r - tok * group);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (static_cast<int64_t>(seq.first + tok) * a.n_heads + qh) * D + c * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 v = __ldg(src + i);
+          raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) raw[i] = 0u;
+      }
+      uint32_t mag = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) mag = __vmaxu2(mag, raw[i] & 0x7FFF7FFFu);
+      mag = max(mag & 0xFFFFu, mag >> 16);
+      mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
+      mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
+      // 2^qe q lies below 2^14; qe is kept where both powers are normal
+      const int qe = min(126, max(-120, 13 + 127 - static_cast<int>(mag >> 7)));
+      const float up = __uint_as_float(static_cast<uint32_t>(qe + 127) << 23);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
+#pragma unroll
+      for (int i = 0; i < kKs; ++i) {
+        qf[nt][i][0] = pack_f16x2(bf16_lo(raw[2 * i]) * up, bf16_hi(raw[2 * i]) * up);
+        qf[nt][i][1] = pack_f16x2(bf16_lo(raw[2 * i + 1]) * up, bf16_hi(raw[2 * i + 1]) * up);
+      }
+      const float f = down * p.scale_log2;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        fac[nt][j] = __shfl_sync(0xFFFFFFFFu, f, (2 * c + j) * 4);
+        const int rr = row0 + nt * 8 + 2 * c + j;
+        lim[nt][j] = rr < n_rows ? start + rr / group + 1 : 0;  // keys the row sees
+      }
+    }
+
+    float o[kMt][NT][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int i = 0; i < kMt; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[nt][j] = -INFINITY;
+        l[nt][j] = 0.f;
+      }
+    const int full_below = start + row0 / group + 1;  // tokens before this are seen by every row of the tile
+
+    // ---- the segment's tokens, kChunk steps at a time
+    for (int cu = t0; alive && cu < t1; cu += kChunk) {
+      const int steps_max = min(kChunk, t1 - cu);
+      // lane i: page, place and exponents of step i
+      int row_of = -1, ek = 0, ev = 0;
+      {
+        const int t = (cu + lane) * kUnit + warp * kTile;
+        if (lane < steps_max && t < keys) {
+          const int pg = __ldg(a.table + static_cast<int64_t>(s) * a.max_pages + t / a.page);
+          if (pg >= 0 && pg < a.n_pages) {
+            const int64_t ph = static_cast<int64_t>(pg) * a.n_kv + head;
+            row_of = static_cast<int>(ph * a.page + t % a.page);
+            ek = static_cast<int>(__ldg(p.ks + ph)) - 127;
+            ev = static_cast<int>(__ldg(p.vs + ph)) - 127;
+          } else {
+            raise_status(kStatusBadIndex);
+          }
+        }
+      }
+      const uint32_t have = __ballot_sync(0xFFFFFFFFu, row_of >= 0);  // steps with something to read
+      uint32_t to_issue = have, to_use = have;
+      auto issue = [&](uint32_t st) {
+        const int i = __ffs(to_issue) - 1;
+        to_issue &= to_issue - 1;
+        const int r = __shfl_sync(0xFFFFFFFFu, row_of, i);
+        if (lane == 0) {
+          uint8_t* dst = ring + st * Cfg::kStageBytes;
+          mbar_arrive_expect_tx(&ctl->full[warp][st], Cfg::kStageBytes);
+          tma_load_2d(dst, &tmK, &ctl->full[warp][st], 0, r);
+          tma_load_2d(dst + Cfg::kTileBytes, &tmV, &ctl->full[warp][st], 0, r);
+        }
+      };
+      uint32_t ahead = stage;
+      for (int i = 0; i < Cfg::kStages && to_issue; ++i) {
+        issue(ahead);
+        ahead = ahead + 1 == Cfg::kStages ? 0 : ahead + 1;
+      }
+      while (to_use) {
+        const int i = __ffs(to_use) - 1;
+        to_use &= to_use - 1;
+        const int ekb = __shfl_sync(0xFFFFFFFFu, ek, i), evb = __shfl_sync(0xFFFFFFFFu, ev, i);
+        const int tb = (cu + i) * kUnit + warp * kTile;  // first token of the step
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[warp][stage], phase, &ctl->abort_flag))) {
+          alive = false;
+          break;
+        }
+        uint8_t* kt = ring + stage * Cfg::kStageBytes;
+        const uint32_t ka = smem_u32(kt), va = ka + Cfg::kTileBytes;
+        if (tb + kTile > seq.len) {
+          // rows past the sequence's end hold anything, a NaN too: their values become zeros
+          // (their scores are masked below)
+          for (int e = lane; e < kTile * (D / 16); e += 32) {
+            const int r = e / (D / 16);
+            if (tb + r >= seq.len) *reinterpret_cast<uint4*>(kt + Cfg::kTileBytes + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the slot is copied into again
+        }
+
+        // ---- S^T: tokens g, g + 8 of the tile; this lane's codes are dimensions D / 4 c ..
+        float z[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[nt][j] = 0.f;
+#pragma unroll
+        for (int v = 0; v < kQr; ++v) {
+          const uint4 x0 = lds128(ka + swz<D>(g, kQr * c + v)), x1 = lds128(ka + swz<D>(g + 8, kQr * c + v));
+          const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const uint32_t a0 = e4m3x2_f16(w0[i4] & 0xFFFFu), a2 = e4m3x2_f16(w0[i4] >> 16);
+            const uint32_t a1 = e4m3x2_f16(w1[i4] & 0xFFFFu), a3 = e4m3x2_f16(w1[i4] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(z[nt], a0, a1, a2, a3, qf[nt][4 * v + i4][0], qf[nt][4 * v + i4][1]);
+          }
+        }
+
+        // ---- softmax: u = z log2(e) sm_scale 2^ek + ev
+        const float fk = __uint_as_float(static_cast<uint32_t>(min(max(ekb, -126), 127) + 127) << 23);
+        const float fe = static_cast<float>(evb);
+        const float back = __uint_as_float(static_cast<uint32_t>(min(max(-evb, -126), 127) + 127) << 23);  // 2^-ev
+        const bool masked = tb + kTile > full_below;
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float top[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float f = fac[nt][j] * fk;
+            z[nt][j] = fmaf(z[nt][j], f, fe);
+            z[nt][2 + j] = fmaf(z[nt][2 + j], f, fe);
+            if (masked) {
+              if (tb + g >= lim[nt][j]) z[nt][j] = -INFINITY;
+              if (tb + g + 8 >= lim[nt][j]) z[nt][2 + j] = -INFINITY;
+            }
+            top[j] = fmaxf(z[nt][j], z[nt][2 + j]);
+            top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 4));
+            top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 8));
+            top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 16));
+          }
+          if (__any_sync(0xFFFFFFFFu, top[0] > m[nt][0] || top[1] > m[nt][1])) {
+            float sc[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float mn = fmaxf(m[nt][j], top[j]);
+              sc[j] = mn == -INFINITY ? 1.0f : ex2(m[nt][j] - mn);
+              m[nt][j] = mn;
+              l[nt][j] *= sc[j];
+            }
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt) {
+              o[mt][nt][0] *= sc[0];
+              o[mt][nt][1] *= sc[1];
+              o[mt][nt][2] *= sc[0];
+              o[mt][nt][3] *= sc[1];
+            }
+          }
+          float pr[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float base = m[nt][j] == -INFINITY ? 0.0f : m[nt][j];  // no key yet: 2^(-inf) = 0
+            pr[j] = ex2(z[nt][j] - base);
+            pr[2 + j] = ex2(z[nt][2 + j] - base);
+            l[nt][j] = fmaf(pr[j] + pr[2 + j], back, l[nt][j]);
+          }
+          pb[nt][0] = movmatrix(pack_f16x2(pr[0], pr[1]));
+          pb[nt][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
+        }
+
+        // ---- O^T += V^T P^T, 16 dimensions (one 16-byte chunk of the rows) at a time
+#pragma unroll
+        for (int mt = 0; mt < kMt; mt += 2) {
+          uint32_t r[4];
+          ldmatrix_x4_trans(r, va + swz<D>(8 * ((lane >> 3) & 1) + (lane & 7), mt + (lane >> 4)));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = __byte_perm(r[2 * h], 0u, 0x3120), hi = __byte_perm(r[2 * h + 1], 0u, 0x3120);
+            const uint32_t a0 = e4m3x2_f16(lo & 0xFFFFu), a1 = e4m3x2_f16(lo >> 16);
+            const uint32_t a2 = e4m3x2_f16(hi & 0xFFFFu), a3 = e4m3x2_f16(hi >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[mt + h][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          }
+        }
+        __syncwarp();  // the slot has been read
+        if (to_issue) issue(stage);
+        if (++stage == Cfg::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!alive) {
+        // a wait gave up: copies in flight (this step's and those issued ahead) land before the block may end
+        uint32_t st = stage, ph = phase;
+        for (int left = __popc(to_use) + 1 - __popc(to_issue); left > 0; --left) {
+          mbar_wait_drain(&ctl->full[warp][st], ph);
+          if (++st == Cfg::kStages) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+        break;
+      }
+    }
+
+    // ---- join the warps: maximum and sum of every row, then the sums of 32 dimensions a round
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], x);
+        if (g == 0) {
+          ctl->m[warp][nt * 8 + 2 * c + j] = m[nt][j];
+          ctl->l[warp][nt * 8 + 2 * c + j] = l[nt][j];
+        }
+      }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == item_units;
+    float* slot = p.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * Cfg::kSlotFloats;
+    float wf[NT][2];  // this warp's factor to the block's maximum
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ctl->m[w][nt * 8 + 2 * c + j]);
+        wf[nt][j] = m[nt][j] == -INFINITY ? 0.0f : ex2(m[nt][j] - mx);
+      }
+    constexpr int kPer = kRows * Cfg::kJoinDims / kThreads > 0 ? kRows * Cfg::kJoinDims / kThreads : 1;
+    // the row sum and maximum that this thread's outputs need (its rows are the same each round)
+    float inv[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = (threadIdx.x + i * kThreads) / Cfg::kJoinDims;
+      float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ctl->m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += ctl->m[w][r] == -INFINITY ? 0.0f : ctl->l[w][r] * ex2(ctl->m[w][r] - mx);
+      inv[i] = sum > 0.0f ? 1.0f / sum : 0.0f;
+      if (threadIdx.x % Cfg::kJoinDims == 0) {
+        if (!whole) {
+          slot[kRows * D + 2 * r] = mx;
+          slot[kRows * D + 2 * r + 1] = sum;
+        } else if (p.lse && row0 + r < n_rows) {
+          const int rr = row0 + r, tok = rr / group;
+          p.lse[static_cast<int64_t>(seq.first + tok) * a.n_heads + head * group + (rr - tok * group)] =
+              sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+    }
+#pragma unroll
+    for (int d0 = 0; d0 < D; d0 += Cfg::kJoinDims) {
+#pragma unroll
+      for (int mt = 0; mt < Cfg::kJoinDims / 16; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int k = d0 / 16 + mt;
+            *reinterpret_cast<float2*>(join + (warp * kRows + nt * 8 + 2 * c + j) * Cfg::kJoinStride + 16 * mt + 2 * g) =
+                make_float2(o[k][nt][j] * wf[nt][j], o[k][nt][2 + j] * wf[nt][j]);
+          }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x + i * kThreads;
+        const int r = e / Cfg::kJoinDims, d = e % Cfg::kJoinDims;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += join[(w * kRows + r) * Cfg::kJoinStride + d];
+        if (!whole) {
+          slot[r * D + d0 + d] = sum;
+        } else if (row0 + r < n_rows) {
+          const int rr = row0 + r, tok = rr / group;
+          p.out[(static_cast<int64_t>(seq.first + tok) * a.n_heads + head * group + (rr - tok * group)) * D + d0 + d] =
+              __bfloat16_as_ushort(__float2bfloat16_rn(sum * inv[i]));
+        }
+      }
+      __syncthreads();
+    }
+    if (!whole && t0 == 0 && threadIdx.x == 0)
+      p.desc[blockIdx.x] = make_int4(s, rt, head, static_cast<int>((first_unit + item_units - 1) / quota));
+
+    // ---- next item
+    at = first_unit + t1;
+    if (at >= u_end) break;
+    if (++head == a.n_kv) {
+      head = 0;
+      item0 = at;
+      if (++rt >= row_tiles(seq, kRows, group)) {
+        rt = 0;
+        do {
+          seq = load_seq(a, ++s);
+        } while (seq.n_new == 0 && s + 1 < a.S);
+      }
+      item_units = units_of(tile_keys(seq, rt, kRows, group));
+    }
+  }
+}
+
+// Joins the parts of a row tile that several blocks computed: block b holds its first
+// part (the end of b's run), blocks b + 1 .. last the others (the beginnings of theirs).
+template <int D, int NT>
+__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnParams p) {
+  using Cfg = AttnCfg<D, NT>;
+  constexpr int kRows = Cfg::kRows;
+  const int4 item = p.desc[blockIdx.x];
+  if (item.x < 0) return;
+  const Kv8Args& a = p.a;
+  const Seq seq = load_seq(a, item.x);
+  const int group = a.n_heads / a.n_kv;
+  const int row0 = item.y * kRows, n_rows = min(kRows, seq.n_new * group - row0);
+  const int first = blockIdx.x, parts = item.w - first + 1;
+  const float* base = p.slots;
+  auto part = [&](int i) {
+    return base + (static_cast<int64_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * Cfg::kSlotFloats;
+  };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp; r < n_rows; r += 4) {
+    float mx = -INFINITY;
+    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, part(i)[kRows * D + 2 * r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    float sum = 0.0f, acc[D / 32];
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) acc[d] = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+      const float* q = part(i);
+      const float pm = q[kRows * D + 2 * r];
+      const float f = pm == -INFINITY ? 0.0f : ex2(pm - mx);
+      sum = fmaf(q[kRows * D + 2 * r + 1], f, sum);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(q[r * D + 32 * d + lane], f, acc[d]);
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int rr = row0 + r, tok = rr / group;
+    const int64_t o = static_cast<int64_t>(seq.first + tok) * a.n_heads + item.z * group + (rr - tok * group);
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) p.out[o * D + 32 * d + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[d] * inv));
+    if (p.lse && lane == 0) p.lse[o] = sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+// rows of a tile: the fewest of 8, 16, 32 that hold the longest sequence's rows
+int tiles_of(const Kv8Args& a) {
+  const int64_t rows = static_cast<int64_t>(a.max_new) * (a.n_heads / a.n_kv);
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
+
+template <int D, int NT>
+cudaError_t launch(AttnParams p, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, cudaStream_t stream) {
+  using Cfg = AttnCfg<D, NT>;
+  const int blocks = num_sms() * Cfg::kBlocksPerSm;
+  const int smem = Cfg::kRingBytes + Cfg::kJoinBytes + static_cast<int>(sizeof(AttnCtl)) + (p.a.S + 1) * 4 + 1024;
+  if (smem > 227 * 1024) return cudaErrorInvalidValue;
+  p.desc = static_cast<int4*>(workspace);
+  p.slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16 * static_cast<size_t>(blocks));
+  auto kern = attn_kv8_kernel<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  {
+    LaunchScope scope(stream, "attn_kv8_kernel");
+    kern<<<blocks, kThreads, smem, stream>>>(tmK, tmV, p);
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  {
+    LaunchScope scope(stream, "attn_kv8_join_kernel");
+    attn_kv8_join_kernel<D, NT><<<blocks, 128, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <int D, int NT>
+size_t workspace_of() {
+  using Cfg = AttnCfg<D, NT>;
+  return static_cast<size_t>(num_sms()) * Cfg::kBlocksPerSm * (16 + 2 * Cfg::kSlotFloats * 4);
+}
+
+}  // namespace
+
+size_t attn_kv8_workspace(const Kv8Args& a) {
+  const int nt = tiles_of(a);
+  if (a.head_dim == 128) return nt == 1 ? workspace_of<128, 1>() : nt == 2 ? workspace_of<128, 2>() : workspace_of<128, 4>();
+  return nt == 1 ? workspace_of<64, 1>() : nt == 2 ? workspace_of<64, 2>() : workspace_of<64, 4>();
+}
+
+cudaError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, float sm_scale, const uint8_t* k_pages,
+                            const uint8_t* v_pages, const uint8_t* k_scales, const uint8_t* v_scales, uint16_t* out,
+                            float* lse, void* workspace, cudaStream_t stream) {
+  AttnParams p{};
+  p.a = a;
+  p.q = q;
+  p.ks = k_scales;
+  p.vs = v_scales;
+  p.out = out;
+  p.lse = lse;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  const uint64_t rows = static_cast<uint64_t>(a.n_pages) * a.n_kv * a.page;
+  const CUtensorMapSwizzle sw = a.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  CUtensorMap tmK, tmV;
+  cudaError_t e = make_tmap_2d(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, k_pages, rows, a.head_dim, a.head_dim, kTile, sw);
+  if (e == cudaSuccess) e = make_tmap_2d(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, v_pages, rows, a.head_dim, a.head_dim, kTile, sw);
+  if (e != cudaSuccess) return e;
+  const int nt = tiles_of(a);
+  if (a.head_dim == 128)
+    return nt == 1   ? launch<128, 1>(p, tmK, tmV, workspace, stream)
+           : nt == 2 ? launch<128, 2>(p, tmK, tmV, workspace, stream)
+                     : launch<128, 4>(p, tmK, tmV, workspace, stream);
+  return nt == 1   ? launch<64, 1>(p, tmK, tmV, workspace, stream)
+         : nt == 2 ? launch<64, 2>(p, tmK, tmV, workspace, stream)
+                   : launch<64, 4>(p, tmK, tmV, workspace, stream);
+}
+
+}  // namespace ar

@@ -16,6 +16,7 @@ namespace ar {
 enum : unsigned int {
   kStatusNonFinite = 1u << 0,  // a NaN/Inf input or gradient was seen
   kStatusTimeout = 1u << 1,    // a pipeline wait gave up after its time limit
+  kStatusBadIndex = 1u << 2,   // a page number or sequence bound read on the device was out of range
 };
 
 extern __device__ unsigned int g_status;

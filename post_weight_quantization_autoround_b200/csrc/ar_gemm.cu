@@ -1208,6 +1208,17 @@ cudaError_t launch_gemm_store_bf16_kmn(const uint16_t* A, const uint16_t* B_kn, 
   return run<false, true, EPI_STORE_BF16, 1, kPairCG>(A, B_kn, p, stream, "umma_gemm<K,MN,store_bf16,pair>");
 }
 
+cudaError_t launch_gemm_store_bf16(const uint16_t* A, const uint16_t* B, uint16_t* out, int M, int N, int K,
+                                   cudaStream_t stream) {
+  // out [M][N] bf16 = A [M][K] B [N][K]^T
+  Params p{};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.Dbf = out;
+  return run<false, false, EPI_STORE_BF16, 1, kPairCG>(A, B, p, stream, "umma_gemm<K,K,store_bf16,pair>");
+}
+
 cudaError_t launch_loss_reduce(const double* partials, int n, int steps, double inv_count, float* loss,
                                cudaStream_t stream) {
   {

@@ -125,6 +125,9 @@ cudaError_t launch_gemm_resadd(const uint16_t* A, const uint16_t* W, const uint1
 // out [M][N] bf16 = A [M][K] B, B stored [K][N]
 cudaError_t launch_gemm_store_bf16_kmn(const uint16_t* A, const uint16_t* B_kn, uint16_t* out, int M, int N, int K,
                                        cudaStream_t stream);
+// out [M][N] bf16 = A [M][K] B [N][K]^T
+cudaError_t launch_gemm_store_bf16(const uint16_t* A, const uint16_t* B, uint16_t* out, int M, int N, int K,
+                                   cudaStream_t stream);
 // causal attention per sample and head over qkv [S*L][3H] (Q, K rotated; V): O [S*L][H] bf16, lse [S][nh][L]
 cudaError_t launch_attn_fwd(const uint16_t* qkv, int S, int L, int H, int head_dim, uint16_t* out, float* lse,
                             cudaStream_t st);
@@ -192,6 +195,37 @@ cudaError_t launch_qdq_nvfp4(const uint16_t* W, const float* V, const float* alp
 cudaError_t launch_fold_nvfp4(const float* dW, const uint16_t* W, float* V, float* alpha, int64_t n, const float* amax,
                               float lr, float v_min, float v_max, float c_min, float c_max, float* dV_out,
                               float* da_out, cudaStream_t stream);
+// MXFP4 (ar_mxfp4.cu): QDQ, straight-through backward, backward + SignSGD update, expansion to bf16
+cudaError_t launch_qdq_mxfp4(const uint16_t* W, const float* V, const float* alpha, int64_t n, uint16_t* W_hat,
+                             uint8_t* codes, uint8_t* scales, cudaStream_t stream);
+cudaError_t launch_bwd_mxfp4(const float* dW, const uint16_t* W, const float* V, const float* alpha, int64_t n,
+                             float* dV_out, float* da_out, cudaStream_t stream);
+cudaError_t launch_fold_mxfp4(const float* dW, const uint16_t* W, float* V, float* alpha, int64_t n, float lr,
+                              float v_min, float v_max, float c_min, float c_max, float* dV_out, float* da_out,
+                              cudaStream_t stream);
+cudaError_t launch_expand_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t n, uint16_t* out,
+                                cudaStream_t stream);
+// MXFP4 weights (E2M1 codes uint8 [N][K/2], E8M0 scales uint8 [N][K/32]), any T, K % 32 == 0: the tcgen05
+// dequant GEMM (ar_w4a16_tc.cu)
+cudaError_t launch_mxfp4_tc(const uint16_t* A, int T, const uint8_t* codes, const uint8_t* scales, int N, int K,
+                            uint16_t* out, cudaStream_t stream);
+// ---- the paged 8-bit cache (ar_kv8.cu, ar_attn_kv8.cu) ----
+struct Kv8Args {
+  const int32_t* cu;     // [S + 1] first new token of each sequence
+  const int32_t* lens;   // [S] tokens of each sequence, the new ones included
+  const int32_t* table;  // [S][max_pages]
+  int64_t T;             // rows of the new tokens' arrays
+  int S, n_heads, n_kv, head_dim, page, max_pages, max_new;
+  int64_t n_pages;
+};
+constexpr int kKv8MaxSeqs = 4096;
+cudaError_t launch_kv8_append(const Kv8Args& a, const uint16_t* qkv, double rope_base, uint8_t* k_pages,
+                              uint8_t* v_pages, uint8_t* k_scales, uint8_t* v_scales, uint16_t* q_out,
+                              cudaStream_t stream);
+size_t attn_kv8_workspace(const Kv8Args& a);
+cudaError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, float sm_scale, const uint8_t* k_pages,
+                            const uint8_t* v_pages, const uint8_t* k_scales, const uint8_t* v_scales, uint16_t* out,
+                            float* lse, void* workspace, cudaStream_t stream);
 // minibatch assembly (ar_gather.cu): n <= kMaxGatherSamples samples of sample_bytes each
 constexpr int kMaxGatherSamples = 64;
 cudaError_t launch_gather_samples(const void* src, int64_t sample_bytes, const int32_t* idx, int n, void* dst,

@@ -1,0 +1,405 @@
+"""The paged 8-bit cache on the GPU against the 64-bit oracle.
+
+Append: values go from bf16 to E4M3 with an exact power-of-two scale, so their codes are equal.  Keys pass the
+rotation in fp32 (two products and a sum: 3 * 2^-24, cosine and sine another 2 * 2^-24 each, of |a| + |b|, taken as
+2^-21), so a key's code may be the neighbour where the exact value lies that near a border: the value read back is
+within half a step (2^-4 relative, 2^-10 of the scale for subnormal codes) plus that.
+
+Attention: P is f16 (2^-11 relative half a step, 2^-25 absolute where it is subnormal), the exponent carries fp32
+errors of z: sums over d / 16 steps and the scaling, at most 16 * 2^-23 of the largest sum of magnitudes, times ln 2
+by the exponential (2^-22 more); the output rounds to bf16 (2^-8)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import lowbit_oracle as L
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ar():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import post_weight_quantization_autoround_b200 as m
+    return m
+
+
+class Cache:
+    """A batch's cache: random valid codes everywhere or, with garbage, arbitrary bytes (NaN codes among them) past the
+    sequences' ends; a table of pages in random order, -1 past the last one."""
+
+    def __init__(self, lens, n_heads, n_kv, d, page, seed, garbage=True, spread=3, max_pages=None):
+        rng = np.random.default_rng(seed)
+        self.rng, self.lens, self.n_heads, self.n_kv, self.d, self.page = rng, list(lens), n_heads, n_kv, d, page
+        used = [-(-n // page) for n in lens]
+        width = max_pages or max(1, max(used))
+        total = sum(used) + 3
+        order = rng.permutation(total)
+        self.table = np.full((len(lens), width), -1, np.int32)
+        at = 0
+        for s, u in enumerate(used):
+            self.table[s, :u] = order[at:at + u]
+            at += u
+        shape = (total, n_kv, page, d)
+        self.k, self.v = (L.e4m3_codes(rng.normal(0, 100, shape)) for _ in range(2))
+        self.ks, self.vs = (rng.integers(120 - spread, 121 + spread, (total, n_kv)).astype(np.uint8) for _ in range(2))
+        if garbage:
+            free = np.ones((total, page), bool)
+            for s, n in enumerate(lens):
+                for j in range(n):
+                    free[self.table[s, j // page], j % page] = False
+            for x in (self.k, self.v):
+                x.transpose(0, 2, 1, 3)[free] = rng.integers(0, 256, (free.sum(), n_kv, d), dtype=np.uint8)
+                x.transpose(0, 2, 1, 3)[free, :, ::3] = 0x7F
+
+    def gpu(self):
+        return [torch.from_numpy(x.copy()).cuda() for x in (self.k, self.v, self.ks, self.vs)]
+
+
+def _index(news, lens):
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    return cu, torch.from_numpy(cu).cuda(), torch.tensor(list(lens), dtype=torch.int32, device="cuda")
+
+
+def _workspace(ar, c, T, max_new):
+    n = ar.ar_attention_kv8_workspace(T, len(c.lens), max_new, c.n_heads, c.n_kv, c.d, c.page, c.k.shape[0], c.table.shape[1])
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def _attend(ar, c, q, cu, lens, max_new, gpu=None, rows=None, lse=None, ws=None, scale=0.0):
+    k, v, ks, vs = gpu or c.gpu()
+    out = torch.full_like(q, 7.0)
+    ws = _workspace(ar, c, q.shape[0], max_new) if ws is None else ws
+    ar.ar_attention_kv8(q, cu, lens, torch.from_numpy(c.table).cuda(), k, v, ks, vs, out, max_new, ws, lse=lse, sm_scale=scale)
+    return out
+
+
+def _check(c, q, cu, out, lse=None, scale=None):
+    T = cu[-1]
+    ref, rl, mag, units, zmag = L.kv8_attention(q[:T].double().cpu().numpy(), cu, c.lens, c.table, c.k, c.v, c.ks, c.vs, c.n_heads, scale)
+    got = out[:T].double().cpu().numpy().reshape(ref.shape)
+    zerr = (16 * 2.0 ** -23 * zmag + 2.0 ** -21)[..., None]
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2 * zerr) * mag + 2.0 ** -25 * units + 1e-30
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3], got[bad][:4], ref[bad][:4], tol[bad][:4])
+    if lse is not None:
+        l = lse[:T].double().cpu().numpy()
+        assert np.array_equal(np.isinf(l), np.isinf(rl))
+        f = np.isfinite(rl)
+        assert (np.abs(l[f] - rl[f]) <= zerr[..., 0][f] + 2.0 ** -21 * (2 + np.abs(rl[f]))).all()
+
+
+SHAPES = [(8, 8, 128), (8, 1, 128), (10, 2, 64), (14, 2, 128), (16, 1, 128), (32, 1, 64), (40, 1, 128), (5, 5, 64)]
+
+
+@pytest.mark.parametrize("n_heads,n_kv,d", SHAPES)
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_attention_one_token(ar, n_heads, n_kv, d, page):
+    lens = [1, 2, 15, 16, 17, 31, 33, 64, 127, 128, 129, 200, 513]
+    c = Cache(lens, n_heads, n_kv, d, page, n_heads + page)
+    cu, cud, ld = _index([1] * len(lens), lens)
+    q = torch.from_numpy(c.rng.normal(size=(len(lens), n_heads * d)).astype(np.float32)).bfloat16().cuda()
+    lse = torch.empty(len(lens), n_heads, device="cuda")
+    out = _attend(ar, c, q, cud, ld, 1, lse=lse)
+    _check(c, q, cu, out, lse)
+    assert ar.ar_get_device_status() == ar.AR_OK and "attn_kv8_kernel" in ar.ar_last_kernels()
+
+
+@pytest.mark.parametrize("n_heads,n_kv,d,page", [(8, 2, 128, 16), (14, 2, 64, 64), (4, 4, 128, 128), (8, 1, 64, 32)])
+def test_attention_ragged_chunks(ar, n_heads, n_kv, d, page):
+    """Several new tokens a sequence, none, a whole prompt, more than the cache holds (rows that see no key), an empty
+    sequence; rows behind the last one stay as they were."""
+    news = [3, 0, 40, 1, 9, 5, 0, 33, 1]
+    lens = [130, 77, 40, 500, 4, 260, 0, 300, 0]
+    c = Cache(lens, n_heads, n_kv, d, page, d + page)
+    cu, cud, ld = _index(news, lens)
+    T = cu[-1] + 5
+    q = torch.from_numpy(c.rng.normal(size=(T, n_heads * d)).astype(np.float32)).bfloat16().cuda()
+    lse = torch.full((T, n_heads), 3.0, device="cuda")
+    out = _attend(ar, c, q, cud, ld, 40, lse=lse)
+    _check(c, q, cu, out, lse)
+    empty = slice(cu[4], cu[4] + 5)  # nine new tokens, four keys
+    assert not out[empty].any() and lse[empty].isneginf().all() and not out[cu[8]].any()
+    assert (out[cu[-1]:] == 7.0).all() and (lse[cu[-1]:] == 3.0).all()
+    # a bound on the new tokens that is too small changes the tile, not the answer
+    _check(c, q, cu, _attend(ar, c, q, cud, ld, 1))
+    assert ar.ar_get_device_status() == ar.AR_OK
+
+
+@pytest.mark.parametrize("n_heads,n_kv,d,lens", [(1, 1, 128, [40001]), (8, 1, 64, [20000, 5, 9000]), (16, 1, 128, [17000]),
+                                                 (32, 1, 128, [9001, 1])])
+def test_attention_split_over_blocks(ar, n_heads, n_kv, d, lens):
+    """Few rows over a long axis: row tiles that many blocks share; twice the same answer, and in a graph whose lengths
+    change between replays."""
+    c = Cache(lens, n_heads, n_kv, d, 64, 5, max_pages=700)
+    cu, cud, ld = _index([1] * len(lens), lens)
+    q = torch.from_numpy(c.rng.normal(size=(len(lens), n_heads * d)).astype(np.float32)).bfloat16().cuda()
+    gpu = c.gpu()
+    out = _attend(ar, c, q, cud, ld, 1, gpu)
+    _check(c, q, cu, out)
+    assert torch.equal(out, _attend(ar, c, q, cud, ld, 1, gpu))
+    ws, got, table = _workspace(ar, c, len(lens), 1), torch.empty_like(q), torch.from_numpy(c.table).cuda()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ar.ar_attention_kv8(q, cud, ld, table, *gpu, got, 1, ws)
+    g.replay()
+    assert torch.equal(out, got)
+    c.lens[0] //= 3
+    ld[0] = c.lens[0]
+    g.replay()
+    torch.cuda.synchronize()
+    _check(c, q, cu, got)
+
+
+def test_attention_scales_that_differ_widely(ar):
+    """Value scales 2^20 apart between pages, key scales that make some scores large: the weights' f16 rounding stays
+    relative to the largest contribution."""
+    lens = [400, 90]
+    c = Cache(lens, 8, 2, 128, 16, 8)
+    c.vs[:] = c.rng.integers(100, 121, c.vs.shape)
+    c.ks[:] = c.rng.integers(116, 121, c.ks.shape)
+    cu, cud, ld = _index([1, 1], lens)
+    q = torch.from_numpy(c.rng.normal(size=(2, 1024)).astype(np.float32)).bfloat16().cuda()
+    _check(c, q, cu, _attend(ar, c, q, cud, ld, 1))
+    # queries far from 1, and zero
+    for f in (2.0 ** -60, 0.0):
+        qs = (q.double() * f).bfloat16()
+        _check(c, qs, cu, _attend(ar, c, qs, cud, ld, 1))
+    qs = (q.double() * 2.0 ** 60).bfloat16()
+    _check(c, qs, cu, _attend(ar, c, qs, cud, ld, 1, scale=2.0 ** -64), scale=2.0 ** -64)
+
+
+def test_attention_non_finite_query_stays_in_its_row(ar):
+    lens = [60, 70]
+    c = Cache(lens, 8, 1, 128, 32, 2)
+    cu, cud, ld = _index([1, 1], lens)
+    q = torch.from_numpy(c.rng.normal(size=(2, 1024)).astype(np.float32)).bfloat16().cuda()
+    want = _attend(ar, c, q, cud, ld, 1)
+    q[0, 130] = float("nan")
+    got = _attend(ar, c, q, cud, ld, 1)
+    assert got[0, 128:256].isnan().all()
+    got[0, 128:256] = want[0, 128:256]
+    assert torch.equal(got, want)
+
+
+def test_attention_bad_indices_are_skipped(ar):
+    """Page numbers outside the pool, bounds outside the arrays: raised, and the other sequences come out right."""
+    lens = [100, 100, 100]
+    c = Cache(lens, 8, 2, 64, 16, 4)
+    cu, cud, ld = _index([1, 1, 1], lens)
+    q = torch.from_numpy(c.rng.normal(size=(3, 512)).astype(np.float32)).bfloat16().cuda()
+    want = _attend(ar, c, q, cud, ld, 1)
+    good = c.table.copy()
+    for bad in (-1, c.k.shape[0], 2 ** 31 - 1, -2 ** 31):
+        c.table = good.copy()
+        c.table[1, 2] = bad
+        got = _attend(ar, c, q, cud, ld, 1)
+        assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG
+        assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    c.table = good
+    for bad in (-5, 7 * 16 + 1, 2 ** 31 - 1):
+        ld[1] = bad
+        got = _attend(ar, c, q, cud, ld, 1)
+        assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG
+        assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2]) and (got[1] == 7.0).all()
+    ld[1] = 100
+    for bad in (-1, 9, 2 ** 31 - 1):
+        cud[3] = bad
+        got = _attend(ar, c, q, cud, ld, 1)
+        assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG
+        assert torch.equal(got[:2], want[:2]) and (got[2] == 7.0).all()
+
+
+def _check_keys(c, gpu, keys, qkv):
+    """Keys: their scales equal, their values within half a code's step of the exact rotation."""
+    k, ks = gpu[0].cpu().numpy(), gpu[2].cpu().numpy()
+    for ph, h, at, new in keys:
+        scale = 2.0 ** (int(ks[ph, h]) - 127)
+        got = L.e4m3_values(k[ph, h, at:at + len(new)]) * scale
+        err = 2.0 ** -21 * np.abs(new).max(1, keepdims=True) * 2
+        assert (np.abs(got - new) <= np.maximum(2.0 ** -4 * np.abs(new), 2.0 ** -10 * scale) * (1 + 2.0 ** -20) + err).all()
+
+
+@pytest.mark.parametrize("n_heads,n_kv,d", [(8, 8, 128), (8, 2, 64), (14, 2, 128), (5, 1, 64)])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_append(ar, n_heads, n_kv, d, page):
+    """From one token to several pages a sequence, pages begun before (whose scale grows, or does not), none, far
+    positions; bytes that belong to no new or older token stay."""
+    news = [1, 1, 0, 3, page, page + 1, 2 * page + 7, 1, 1, 5]
+    lens = [1, page + 3, 9, 3, page, 3 * page, 4 * page + 1, page, 6 * page + 2, 5 + page - 2]
+    c = Cache(lens, n_heads, n_kv, d, page, d + page)
+    cu, cud, ld = _index(news, lens)
+    T = cu[-1] + 2
+    qkv = c.rng.normal(size=(T, (n_heads + 2 * n_kv) * d)) * 3
+    qkv[cu[1]:cu[2]] *= 2.0 ** -9  # older tokens keep the larger scale
+    qkv[cu[8]:cu[9]] *= 2.0 ** 13  # older tokens are re-coded
+    qkv = torch.from_numpy(qkv.astype(np.float32)).bfloat16().cuda()
+    gpu = c.gpu()
+    q_out = torch.full((T, n_heads * d), 7.0, dtype=torch.bfloat16, device="cuda")
+    ar.ar_kv8_append(qkv, cud, ld, torch.from_numpy(c.table).cuda(), *gpu, q_out, 2 * page + 7)
+    assert ar.ar_get_device_status() == ar.AR_OK
+    before = c.k.copy()
+    rq, keys = L.kv8_append(qkv.double().cpu().numpy()[:cu[-1]], cu, lens, c.table, c.k, c.v, c.ks, c.vs, n_heads)
+    got = q_out[:cu[-1]].double().cpu().numpy().reshape(rq.shape)
+    assert (np.abs(got - rq) <= 2.0 ** -8 * np.abs(rq) + 2.0 ** -21 * np.abs(rq).max(2, keepdims=True) * 2).all()
+    assert (q_out[cu[-1]:] == 7.0).all()
+    assert np.array_equal(gpu[1].cpu().numpy(), c.v) and np.array_equal(gpu[3].cpu().numpy(), c.vs)
+    assert np.array_equal(gpu[2].cpu().numpy(), c.ks)
+    _check_keys(c, gpu, keys, qkv)
+    k = gpu[0].cpu().numpy()
+    new = np.zeros(k.shape, bool)
+    for ph, h, at, rows in keys:
+        new[ph, h, at:at + len(rows)] = True
+    assert np.array_equal(k[~new], c.k[~new])  # untouched, or re-coded the same
+    assert (before[~new] != c.k[~new]).any() and (k[new] != c.k[new]).mean() < 1e-3
+
+
+def test_append_far_positions(ar):
+    """A position past 10^6: the angle keeps its fraction of a turn."""
+    page, d = 128, 128
+    lens = [1_000_001, 777_777]
+    n_pages = 4
+    table = np.zeros((2, -(-lens[0] // page)), np.int32)
+    table[0, (lens[0] - 1) // page], table[1, (lens[1] - 1) // page] = 1, 2
+    k, v = (np.zeros((n_pages, 1, page, d), np.uint8) for _ in range(2))
+    ks, vs = (np.full((n_pages, 1), 27, np.uint8) for _ in range(2))
+    cu, cud, ld = _index([1, 1], lens)
+    qkv = torch.from_numpy(np.random.default_rng(0).normal(size=(2, 3 * d)).astype(np.float32)).bfloat16().cuda()
+    gpu = [torch.from_numpy(x.copy()).cuda() for x in (k, v, ks, vs)]
+    q_out = torch.empty(2, d, dtype=torch.bfloat16, device="cuda")
+    ar.ar_kv8_append(qkv, cud, ld, torch.from_numpy(table).cuda(), *gpu, q_out, 1, rope_base=500000.0)
+    rq, keys = L.kv8_append(qkv.double().cpu().numpy(), cu, lens, table, k, v, ks, vs, 1, base=500000.0)
+    got = q_out.double().cpu().numpy().reshape(rq.shape)
+    assert (np.abs(got - rq) <= 2.0 ** -8 * np.abs(rq) + 2.0 ** -20 * np.abs(rq).max(2, keepdims=True)).all()
+    _check_keys(None, gpu, keys, qkv)
+
+
+def test_append_non_finite_and_zero(ar):
+    c = Cache([20, 20], 2, 1, 64, 16, 1)
+    cu, cud, ld = _index([4, 4], [20, 20])
+    qkv = torch.from_numpy(c.rng.normal(size=(8, 4 * 64)).astype(np.float32)).bfloat16().cuda()
+    qkv[0, 192], qkv[1, 193], qkv[2, 194] = float("nan"), float("inf"), -float("inf")  # values of the first sequence
+    qkv[4:, 128:] = 0.0  # keys and values of the second
+    gpu = c.gpu()
+    q_out = torch.empty(8, 128, dtype=torch.bfloat16, device="cuda")
+    ar.ar_kv8_append(qkv, cud, ld, torch.from_numpy(c.table).cuda(), *gpu, q_out, 4)
+    assert ar.ar_get_device_status() == ar.AR_ERR_NONFINITE
+    v = gpu[1][c.table[0, 1], 0].cpu().numpy()
+    assert v[0, 0] == 0 and v[1, 1] == 0x7E and v[2, 2] == 0xFE
+    finite = qkv[:4, 192:].double().cpu().numpy()
+    finite[~np.isfinite(finite)] = 0
+    assert gpu[3][c.table[0, 1], 0].item() == L.exponent_for(np.abs(finite).max()) + 127
+    z = c.table[1, 1]
+    # zeros of either sign: a rotation gives 0 * c - 0 * s
+    assert not (gpu[0][z, 0, :4] & 0x7F).any() and not (gpu[1][z, 0, :4] & 0x7F).any() and gpu[2][z, 0] == 27 and gpu[3][z, 0] == 27
+
+
+def test_append_bad_indices_are_skipped(ar):
+    lens = [40, 40, 40]
+    c = Cache(lens, 4, 2, 64, 16, 6)
+    cu, cud, ld = _index([2, 2, 2], lens)
+    qkv = torch.from_numpy(c.rng.normal(size=(6, 8 * 64)).astype(np.float32)).bfloat16().cuda()
+
+    def run(table=c.table, cu_=cud, ld_=ld, max_new=2):
+        gpu = c.gpu()
+        q = torch.full((6, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+        ar.ar_kv8_append(qkv, cu_, ld_, torch.from_numpy(table).cuda(), *gpu, q, max_new)
+        return gpu, q, ar.ar_get_device_status()
+
+    want, wq, st = run()
+    assert st == ar.AR_OK
+    page1 = c.table[1, 2]
+    others = [p for p in range(c.k.shape[0]) if p != page1]
+
+    def same_but_second(got, q, st):
+        assert st == ar.AR_ERR_INVALID_ARG
+        for a, b, orig in zip(got, want, (c.k, c.v, c.ks, c.vs)):
+            assert torch.equal(a[others], b[others]) and np.array_equal(a[page1].cpu().numpy(), orig[page1])
+        assert torch.equal(q[:2], wq[:2]) and torch.equal(q[4:], wq[4:])
+
+    for bad in (-1, c.k.shape[0], 2 ** 31 - 1, -2 ** 31):
+        t = c.table.copy()
+        t[1, 2] = bad
+        same_but_second(*run(table=t))
+    for bad in (1, 3 * 16 + 1, -3, 2 ** 31 - 1):
+        l2 = ld.clone()
+        l2[1] = bad
+        got, q, st = run(ld_=l2)
+        same_but_second(got, q, st)
+        assert (q[2:4] == 7.0).all()
+    for bad in (7, -1, 2 ** 31 - 1):
+        c2 = cud.clone()
+        c2[3] = bad
+        got, q, st = run(cu_=c2)
+        assert st == ar.AR_ERR_INVALID_ARG and torch.equal(q[:4], wq[:4]) and (q[4:] == 7.0).all()
+    assert run(max_new=1)[2] == ar.AR_ERR_INVALID_ARG  # every sequence has two
+
+
+def test_two_calls_at_once(ar):
+    """Two streams, a workspace each."""
+    cs = [Cache([900, 33], 8, 2, 128, 32, s) for s in (1, 2)]
+    cu, cud, ld = _index([1, 1], [900, 33])
+    qs = [torch.from_numpy(c.rng.normal(size=(2, 1024)).astype(np.float32)).bfloat16().cuda() for c in cs]
+    gpus = [c.gpu() for c in cs]
+    want = [_attend(ar, c, q, cud, ld, 1, g) for c, q, g in zip(cs, qs, gpus)]
+    ws = [_workspace(ar, c, 2, 1) for c in cs]
+    tables = [torch.from_numpy(c.table).cuda() for c in cs]
+    outs = [torch.empty_like(q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            ar.ar_attention_kv8(qs[i], cud, ld, tables[i], *gpus[i], outs[i], 1, ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs))
+
+
+def test_a_decode_step_of_the_operators_together(ar):
+    """Norm, MXFP4 projection, append, attention, MXFP4 projection: a prompt in two pieces and then token by token gives
+    what the whole prompt at once gives.  Both runs quantize the same keys and values; a page's scale may have grown in
+    steps in one of them, which re-codes exactly unless a code is subnormal, so they agree to E4M3's smallest steps;
+    measured against the outputs' size that is far below the 2^-5 allowed here (bf16 steps of four roundings in a row
+    are 2^-6)."""
+    H, n_heads, n_kv, d, page, L_ = 512, 8, 2, 64, 16, 45
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.randn(L_, H, device="cuda", generator=g).bfloat16()
+    gamma = torch.ones(H, device="cuda")
+
+    def packed(n, k):
+        w = (torch.randn(n, k, device="cuda", generator=g) * 0.05).bfloat16()
+        codes, scales = torch.empty(n, k // 2, dtype=torch.uint8, device="cuda"), torch.empty(n, k // 32, dtype=torch.uint8, device="cuda")
+        ar.ar_qdq_mxfp4(w, codes=codes, scales=scales)
+        return codes, scales
+
+    wqkv, wo = packed((n_heads + 2 * n_kv) * d, H), packed(H, n_heads * d)
+
+    def run(pieces):
+        pages = -(-L_ // page)
+        k, v = (torch.full((pages, n_kv, page, d), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.full((pages, n_kv), 255, dtype=torch.uint8, device="cuda") for _ in range(2))
+        table = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device="cuda").view(1, -1)
+        outs, at = [], 0
+        for n in pieces:
+            r = torch.empty(n, H, dtype=torch.bfloat16, device="cuda")
+            ar.ar_rmsnorm(x[at:at + n].contiguous(), gamma, r)
+            qkv = torch.empty(n, (n_heads + 2 * n_kv) * d, dtype=torch.bfloat16, device="cuda")
+            ar.ar_mxfp4_gemm(r, *wqkv, qkv)
+            cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+            at += n
+            lens = torch.tensor([at], dtype=torch.int32, device="cuda")
+            q, o = torch.empty(n, n_heads * d, dtype=torch.bfloat16, device="cuda"), torch.empty(n, n_heads * d, dtype=torch.bfloat16, device="cuda")
+            ar.ar_kv8_append(qkv, cu, lens, table, k, v, ks, vs, q, n)
+            ws = torch.empty(ar.ar_attention_kv8_workspace(n, 1, n, n_heads, n_kv, d, page, pages, pages), dtype=torch.uint8, device="cuda")
+            ar.ar_attention_kv8(q, cu, lens, table, k, v, ks, vs, o, n, ws)
+            y = torch.empty(n, H, dtype=torch.bfloat16, device="cuda")
+            ar.ar_mxfp4_gemm(o, *wo, y)
+            outs.append(y)
+        assert ar.ar_get_device_status() == ar.AR_OK
+        return torch.cat(outs).double(), (k, v, ks, vs)
+
+    whole, ca = run([L_])
+    steps, cb = run([20, 17] + [1] * 8)
+    assert (whole[-1] - steps[-1]).norm() <= 2.0 ** -5 * whole[-1].norm()
+    for a, b in zip(ca[2:], cb[2:]):
+        assert torch.equal(a, b)  # the scales end where the whole prompt put them
