@@ -542,36 +542,37 @@ def ar_attention_backward(qkv, out, dout, lse, S: int, L: int, n_heads: int, dqk
 
 # ---- MXFP4 weights -----------------------------------------------------------
 
-def _typed(t: Optional[torch.Tensor], dtype, shape, name: str, device=None) -> Optional[int]:
-    """``_ptr`` of a tensor of the given type and shape on the current device (None stays None)."""
+def _typed(t: Optional[torch.Tensor], dtype, shape, name: str, device: int) -> Optional[int]:
+    """Address of a contiguous tensor of the given type and shape on the given (current) device; None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ARError(AR_ERR_INVALID_ARG, f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ARError(AR_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current device")
-    return _ptr(t)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ARError(AR_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} {tuple(shape)} on the current CUDA device, "
+                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def ar_qdq_mxfp4(W, V=None, alpha=None, W_hat=None, codes=None, scales=None, stream=None) -> None:
     """MXFP4 fake quantization of W [N][K] (bf16): V [N][K] fp32 or None, alpha [N][K/32] fp32 or None; outputs
     W_hat bf16 [N][K], codes uint8 [N][K/2], scales uint8 [N][K/32] (E8M0 codes), each optional."""
     N, K = W.shape
-    _check(lib().ar_qdq_mxfp4(_typed(W, torch.bfloat16, (N, K), "W"), _typed(V, torch.float32, (N, K), "V"),
-                              _typed(alpha, torch.float32, (N, K // 32), "alpha"), N, K,
-                              _typed(W_hat, torch.bfloat16, (N, K), "W_hat"),
-                              _typed(codes, torch.uint8, (N, K // 2), "codes"),
-                              _typed(scales, torch.uint8, (N, K // 32), "scales"), _stream(stream)))
+    dev = torch.cuda.current_device()
+    _check(lib().ar_qdq_mxfp4(_typed(W, torch.bfloat16, (N, K), "W", dev), _typed(V, torch.float32, (N, K), "V", dev),
+                              _typed(alpha, torch.float32, (N, K // 32), "alpha", dev), N, K,
+                              _typed(W_hat, torch.bfloat16, (N, K), "W_hat", dev),
+                              _typed(codes, torch.uint8, (N, K // 2), "codes", dev),
+                              _typed(scales, torch.uint8, (N, K // 32), "scales", dev), _stream(stream)))
 
 
 def ar_qdq_mxfp4_backward(dW_hat, W, V, alpha, dV=None, dalpha=None, stream=None) -> None:
     """Straight-through gradients of ``ar_qdq_mxfp4``: dV fp32 [N][K], dalpha fp32 [N][K/32] from dW_hat fp32 [N][K]."""
     N, K = W.shape
-    _check(lib().ar_qdq_mxfp4_backward(_typed(dW_hat, torch.float32, (N, K), "dW_hat"),
-                                       _typed(W, torch.bfloat16, (N, K), "W"), _typed(V, torch.float32, (N, K), "V"),
-                                       _typed(alpha, torch.float32, (N, K // 32), "alpha"), N, K,
-                                       _typed(dV, torch.float32, (N, K), "dV"),
-                                       _typed(dalpha, torch.float32, (N, K // 32), "dalpha"), _stream(stream)))
+    dev = torch.cuda.current_device()
+    _check(lib().ar_qdq_mxfp4_backward(_typed(dW_hat, torch.float32, (N, K), "dW_hat", dev),
+                                       _typed(W, torch.bfloat16, (N, K), "W", dev), _typed(V, torch.float32, (N, K), "V", dev),
+                                       _typed(alpha, torch.float32, (N, K // 32), "alpha", dev), N, K,
+                                       _typed(dV, torch.float32, (N, K), "dV", dev),
+                                       _typed(dalpha, torch.float32, (N, K // 32), "dalpha", dev), _stream(stream)))
 
 
 def ar_tune_step_mxfp4_workspace(M: int, N: int, K: int, n_steps: int) -> int:
@@ -587,14 +588,15 @@ def ar_tune_step_mxfp4(W, V, alpha, X, Y, cfg: QConfig, n_steps: int, loss_per_s
     loss_per_step: fp32 device [max(n_steps, 1)]; workspace: uint8 device tensor of
     ``ar_tune_step_mxfp4_workspace`` bytes."""
     N, K = W.shape
+    dev = torch.cuda.current_device()
     M = X.shape[0]
-    _check(lib().ar_tune_step_mxfp4(_typed(W, torch.bfloat16, (N, K), "W"), _typed(V, torch.float32, (N, K), "V"),
-                                    _typed(alpha, torch.float32, (N, K // 32), "alpha"), N, K,
-                                    _typed(X, torch.bfloat16, (M, K), "X"), M, _typed(Y, torch.float32, (M, N), "Y"),
+    _check(lib().ar_tune_step_mxfp4(_typed(W, torch.bfloat16, (N, K), "W", dev), _typed(V, torch.float32, (N, K), "V", dev),
+                                    _typed(alpha, torch.float32, (N, K // 32), "alpha", dev), N, K,
+                                    _typed(X, torch.bfloat16, (M, K), "X", dev), M, _typed(Y, torch.float32, (M, N), "Y", dev),
                                     ctypes.byref(cfg), n_steps,
-                                    _typed(loss_per_step, torch.float32, (max(n_steps, 1),), "loss_per_step"),
-                                    _typed(dV, torch.float32, (N, K), "dV"),
-                                    _typed(dalpha, torch.float32, (N, K // 32), "dalpha"), _ptr(workspace),
+                                    _typed(loss_per_step, torch.float32, (max(n_steps, 1),), "loss_per_step", dev),
+                                    _typed(dV, torch.float32, (N, K), "dV", dev),
+                                    _typed(dalpha, torch.float32, (N, K // 32), "dalpha", dev), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -610,9 +612,10 @@ def ar_mxfp4_gemm(A, codes, scales, out, workspace=None, stream=None) -> None:
     ``ar_qdq_mxfp4`` writes them); workspace: ``ar_mxfp4_gemm_workspace`` bytes, or None."""
     T, K = A.shape
     N = codes.shape[0]
-    _check(lib().ar_mxfp4_gemm(_typed(A, torch.bfloat16, (T, K), "A"), T, _typed(codes, torch.uint8, (N, K // 2), "codes"),
-                               _typed(scales, torch.uint8, (N, K // 32), "scales"), N, K,
-                               _typed(out, torch.bfloat16, (T, N), "out"), _ptr(workspace),
+    dev = torch.cuda.current_device()
+    _check(lib().ar_mxfp4_gemm(_typed(A, torch.bfloat16, (T, K), "A", dev), T, _typed(codes, torch.uint8, (N, K // 2), "codes", dev),
+                               _typed(scales, torch.uint8, (N, K // 32), "scales", dev), N, K,
+                               _typed(out, torch.bfloat16, (T, N), "out", dev), _ptr(workspace),
                                0 if workspace is None else workspace.numel() * workspace.element_size(),
                                _stream(stream)))
 
@@ -623,13 +626,14 @@ def _kv8(cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales,
     """The cache's description and the pointers that both calls take."""
     n_pages, n_kv, page, d = k_pages.shape
     S, max_pages = page_table.shape
+    dev = torch.cuda.current_device()
     cfg = Kv8Cfg(n_heads, n_kv, d, page, n_pages, max_pages)
-    index = (_typed(cu_seqlens, torch.int32, (S + 1,), "cu_seqlens"), _typed(seq_lens, torch.int32, (S,), "seq_lens"),
-             _typed(page_table, torch.int32, (S, max_pages), "page_table"))
+    index = (_typed(cu_seqlens, torch.int32, (S + 1,), "cu_seqlens", dev), _typed(seq_lens, torch.int32, (S,), "seq_lens", dev),
+             _typed(page_table, torch.int32, (S, max_pages), "page_table", dev))
     shape = (n_pages, n_kv, page, d)
-    cache = (_typed(k_pages, torch.uint8, shape, "k_pages"), _typed(v_pages, torch.uint8, shape, "v_pages"),
-             _typed(k_scales, torch.uint8, shape[:2], "k_scales"), _typed(v_scales, torch.uint8, shape[:2], "v_scales"))
-    return cfg, index, cache, S
+    cache = (_typed(k_pages, torch.uint8, shape, "k_pages", dev), _typed(v_pages, torch.uint8, shape, "v_pages", dev),
+             _typed(k_scales, torch.uint8, shape[:2], "k_scales", dev), _typed(v_scales, torch.uint8, shape[:2], "v_scales", dev))
+    return cfg, index, cache, S, dev
 
 
 def ar_kv8_append(qkv, cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, q_out, max_new: int,
@@ -643,10 +647,10 @@ def ar_kv8_append(qkv, cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_sca
     T, width = qkv.shape
     n_kv, d = k_pages.shape[1], k_pages.shape[3]
     n_heads = width // d - 2 * n_kv
-    cfg, index, cache, S = _kv8(cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, n_heads)
-    _check(lib().ar_kv8_append(ctypes.byref(cfg), _typed(qkv, torch.bfloat16, (T, (n_heads + 2 * n_kv) * d), "qkv"), T,
+    cfg, index, cache, S, dev = _kv8(cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, n_heads)
+    _check(lib().ar_kv8_append(ctypes.byref(cfg), _typed(qkv, torch.bfloat16, (T, (n_heads + 2 * n_kv) * d), "qkv", dev), T,
                                *index, S, max_new, rope_base, *cache,
-                               _typed(q_out, torch.bfloat16, (T, n_heads * d), "q_out"), _stream(stream)))
+                               _typed(q_out, torch.bfloat16, (T, n_heads * d), "q_out", dev), _stream(stream)))
 
 
 def ar_attention_kv8_workspace(T: int, S: int, max_new: int, n_heads: int, n_kv_heads: int, head_dim: int,
@@ -664,9 +668,9 @@ def ar_attention_kv8(q, cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_sc
     lse fp32 [T][n_heads] or None; sm_scale 0 is 1/sqrt(d); workspace: ``ar_attention_kv8_workspace`` bytes."""
     T, width = q.shape
     n_heads = width // k_pages.shape[3]
-    cfg, index, cache, S = _kv8(cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, n_heads)
+    cfg, index, cache, S, dev = _kv8(cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_scales, v_scales, n_heads)
     shape = (T, n_heads * k_pages.shape[3])
-    _check(lib().ar_attention_kv8(ctypes.byref(cfg), _typed(q, torch.bfloat16, shape, "q"), T, *index, S, max_new,
-                                  sm_scale, *cache, _typed(out, torch.bfloat16, shape, "out"),
-                                  _typed(lse, torch.float32, (T, n_heads), "lse"), _ptr(workspace),
+    _check(lib().ar_attention_kv8(ctypes.byref(cfg), _typed(q, torch.bfloat16, shape, "q", dev), T, *index, S, max_new,
+                                  sm_scale, *cache, _typed(out, torch.bfloat16, shape, "out", dev),
+                                  _typed(lse, torch.float32, (T, n_heads), "lse", dev), _ptr(workspace),
                                   workspace.numel() * workspace.element_size(), _stream(stream)))

@@ -625,18 +625,20 @@ cudaError_t launch(AttnParams p, const CUtensorMap& tmK, const CUtensorMap& tmV,
   using Cfg = AttnCfg<D, NT>;
   const int blocks = num_sms() * Cfg::kBlocksPerSm;
   const int smem = Cfg::kRingBytes + Cfg::kJoinBytes + static_cast<int>(sizeof(AttnCtl)) + (p.a.S + 1) * 4 + 1024;
-  if (smem > 227 * 1024) return cudaErrorInvalidValue;
+  static_assert(Cfg::kRingBytes + Cfg::kJoinBytes + sizeof(AttnCtl) + (kKv8MaxSeqs + 1) * 4 + 1024 <= 227 * 1024, "shared memory per block");
   p.desc = static_cast<int4*>(workspace);
   p.slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16 * static_cast<size_t>(blocks));
   auto kern = attn_kv8_kernel<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), 227 * 1024, allowed);
   if (e != cudaSuccess) return e;
   {
     LaunchScope scope(stream, "attn_kv8_kernel");
     kern<<<blocks, kThreads, smem, stream>>>(tmK, tmV, p);
   }
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // no item has two units when a sequence cannot pass one: nothing to join
+  if (e != cudaSuccess || static_cast<int64_t>(p.a.max_pages) * p.a.page <= kUnit) return e;
   {
     LaunchScope scope(stream, "attn_kv8_join_kernel");
     attn_kv8_join_kernel<D, NT><<<blocks, 128, 0, stream>>>(p);

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ar_device.cuh"
 
 namespace ar {
@@ -35,6 +37,11 @@ class LaunchScope {
 };
 
 int num_sms();
+
+// Lets a kernel use up to `bytes` of dynamic shared memory on the current device,
+// asking the runtime once per device and kernel (`done` is the caller's, one bit a
+// device: the attribute belongs to the function, not to a call).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 cudaError_t launch_qdq(const uint16_t* W, const float* V, const float* alpha, const float* beta, int64_t N,
                        int64_t K, int group_size, int bits, int symmetric, uint16_t* W_hat, uint8_t* codes,

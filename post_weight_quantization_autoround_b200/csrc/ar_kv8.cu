@@ -21,7 +21,7 @@
 // not depend on timing.  The kernel is bound by memory (read 2 B, write 2 B a query
 // element, read 2 B, write 1 B a key or value element); the block's cosines and sines
 // are computed once in shared memory and serve all its heads, and a token's keys stay
-// in registers between the maximum and the codes.
+// in registers, as loaded, between the maximum and the codes.
 #include <cuda_fp8.h>
 
 #include "ar_internal.h"
@@ -56,41 +56,64 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t two) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3)));
 }
 
-// a lane's 8 elements of a head: 4 of the first half and the 4 they rotate with
-struct Eight {
-  float lo[4], hi[4];
+// a lane's 16 elements of a head as loaded: 8 of the first half and the 8 they rotate with
+struct Raw {
+  uint4 lo, hi;
 };
 
-__device__ __forceinline__ Eight load_eight(const uint16_t* p, int half) {
-  const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
-  const uint2 b = __ldg(reinterpret_cast<const uint2*>(p + half));
-  Eight x;
-  x.lo[0] = bf16_lo(a.x); x.lo[1] = bf16_hi(a.x); x.lo[2] = bf16_lo(a.y); x.lo[3] = bf16_hi(a.y);
-  x.hi[0] = bf16_lo(b.x); x.hi[1] = bf16_hi(b.x); x.hi[2] = bf16_lo(b.y); x.hi[3] = bf16_hi(b.y);
+struct Sixteen {
+  float lo[8], hi[8];
+};
+
+__device__ __forceinline__ Raw load_raw(const uint16_t* p, int half) {
+  return {__ldg(reinterpret_cast<const uint4*>(p)), __ldg(reinterpret_cast<const uint4*>(p + half))};
+}
+
+__device__ __forceinline__ Sixteen values_of(const Raw& r) {
+  const uint32_t a[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w}, b[4] = {r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+  Sixteen x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.lo[2 * i] = bf16_lo(a[i]);
+    x.lo[2 * i + 1] = bf16_hi(a[i]);
+    x.hi[2 * i] = bf16_lo(b[i]);
+    x.hi[2 * i + 1] = bf16_hi(b[i]);
+  }
   return x;
 }
 
-__device__ __forceinline__ void rotate(Eight& x, const float2* cs) {
+__device__ __forceinline__ Sixteen rotated(const Raw& r, const float2* cs) {
+  Sixteen x = values_of(r);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 t = cs[i];
-    const float a = x.lo[i], b = x.hi[i];
-    x.lo[i] = a * t.x - b * t.y;
-    x.hi[i] = b * t.x + a * t.y;
+    const float4 t = *reinterpret_cast<const float4*>(cs + 2 * i);  // two pairs (cos, sin)
+    const float a0 = x.lo[2 * i], b0 = x.hi[2 * i], a1 = x.lo[2 * i + 1], b1 = x.hi[2 * i + 1];
+    x.lo[2 * i] = a0 * t.x - b0 * t.y;
+    x.hi[2 * i] = b0 * t.x + a0 * t.y;
+    x.lo[2 * i + 1] = a1 * t.z - b1 * t.w;
+    x.hi[2 * i + 1] = b1 * t.z + a1 * t.w;
   }
+  return x;
 }
 
-// D: head dimension; PASSES * (threads / (D / 8)) covers a page
+// max(m, |x|), a NaN wins
+__device__ __forceinline__ float max_mag(float m, float x) {
+  float r;
+  asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(m), "f"(x));
+  return r;
+}
+
+// D: head dimension; PASSES * (threads / (D / 16)) covers the new tokens that a page can take
 template <int D, int PASSES, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 512 / THREADS)
     kv8_append_kernel(const Kv8Args a, const uint16_t* __restrict__ qkv, const __grid_constant__ RopeTurns turns,
                       uint8_t* __restrict__ k_pages, uint8_t* __restrict__ v_pages, uint8_t* __restrict__ k_scales,
                       uint8_t* __restrict__ v_scales, uint16_t* __restrict__ q_out, int heads_per_block) {
   constexpr int kHalf = D / 2;
-  constexpr int kLanes = D / 8;              // lanes that share a token's head
+  constexpr int kLanes = D / 16;             // lanes that share a token's head
   constexpr int kTokens = THREADS / kLanes;  // tokens per pass
   constexpr int kWarps = THREADS / 32;
-  extern __shared__ float2 cs[];  // [tokens][D / 2]
+  extern __shared__ __align__(16) float2 cs[];  // [tokens][D / 2]
   __shared__ float warp_max[2][kWarps];
 
   const int s = blockIdx.y;
@@ -124,7 +147,7 @@ __global__ void __launch_bounds__(THREADS)
   }
   __syncthreads();
 
-  const int lane8 = tid % kLanes;  // elements 4 lane8 .. + 3 and D / 2 further
+  const int el = 8 * (tid % kLanes);  // this lane's elements: el .. el + 7 and D / 2 further
   const int tok0 = tid / kLanes;
   const int64_t row0 = first_row + (lo - start);
   const int64_t ld = static_cast<int64_t>(a.n_heads + 2 * a.n_kv) * D;
@@ -133,60 +156,87 @@ __global__ void __launch_bounds__(THREADS)
   const int h1 = min(a.n_kv, h0 + heads_per_block);
   int buf = 0;
 
+  // the largest magnitude over the block (a NaN wins); every thread gets it
+  auto block_max = [&](float top) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max_mag(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if ((tid & 31) == 0) warp_max[buf][tid >> 5] = top;
+    __syncthreads();
+    top = warp_max[buf][0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = max_mag(top, warp_max[buf][w]);
+    buf ^= 1;  // the next maximum is written while this one may still be read
+    return top;
+  };
+
   for (int h = h0; h < h1; ++h) {
-    // queries of the heads that read this one
-    for (int j = tok0; j < n * group; j += kTokens) {
-      const int t = j / group, qh = h * group + (j - t * group);
-      Eight x = load_eight(qkv + (row0 + t) * ld + qh * D + 4 * lane8, kHalf);
-      rotate(x, cs + t * kHalf + 4 * lane8);
-      uint16_t* o = q_out + ((row0 + t) * a.n_heads + qh) * D + 4 * lane8;
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(x.lo[0], x.lo[1]), pack_bf16x2(x.lo[2], x.lo[3]));
-      *reinterpret_cast<uint2*>(o + kHalf) = make_uint2(pack_bf16x2(x.hi[0], x.hi[1]), pack_bf16x2(x.hi[2], x.hi[3]));
+    Raw kv[2][PASSES];  // keys and values: loaded before the queries are worked on
+    if (page_ok) {
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+          const int t = tok0 + p * kTokens;
+          kv[part][p] = t < n ? load_raw(qkv + (row0 + t) * ld + (a.n_heads + part * a.n_kv + h) * D + el, kHalf)
+                              : Raw{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        }
+    }
+    // queries of the heads that read this one, two loads in flight beside the keys' and values'
+    constexpr int kQ = PASSES < 2 ? PASSES : 2;
+    for (int j0 = tok0; j0 < n * group; j0 += kQ * kTokens) {
+      Raw q[kQ];
+#pragma unroll
+      for (int p = 0; p < kQ; ++p) {
+        const int j = j0 + p * kTokens, t = j / group;
+        if (j < n * group) q[p] = load_raw(qkv + (row0 + t) * ld + (h * group + (j - t * group)) * D + el, kHalf);
+      }
+#pragma unroll
+      for (int p = 0; p < kQ; ++p) {
+        const int j = j0 + p * kTokens, t = j / group;
+        if (j >= n * group) continue;
+        const Sixteen x = rotated(q[p], cs + t * kHalf + el);
+        uint16_t* o = q_out + ((row0 + t) * a.n_heads + h * group + (j - t * group)) * D + el;
+        __stcs(reinterpret_cast<uint4*>(o), make_uint4(pack_bf16x2(x.lo[0], x.lo[1]), pack_bf16x2(x.lo[2], x.lo[3]),
+                                                       pack_bf16x2(x.lo[4], x.lo[5]), pack_bf16x2(x.lo[6], x.lo[7])));
+        __stcs(reinterpret_cast<uint4*>(o + kHalf), make_uint4(pack_bf16x2(x.hi[0], x.hi[1]), pack_bf16x2(x.hi[2], x.hi[3]),
+                                                               pack_bf16x2(x.hi[4], x.hi[5]), pack_bf16x2(x.hi[6], x.hi[7])));
+      }
     }
     if (!page_ok) continue;  // uniform over the block
 #pragma unroll
     for (int part = 0; part < 2; ++part) {  // keys, then values
       uint8_t* pages = part == 0 ? k_pages : v_pages;
       uint8_t* scale = (part == 0 ? k_scales : v_scales) + static_cast<int64_t>(physical) * a.n_kv + h;
-      const uint16_t* src = qkv + row0 * ld + (a.n_heads + part * a.n_kv + h) * D + 4 * lane8;
-      Eight x[PASSES];
+      // the values are formed twice, for the maximum and for the codes: holding them would cost a block of occupancy
+      auto value = [&](int p) {
+        const int t = min(tok0 + p * kTokens, n - 1);
+        return part == 0 ? rotated(kv[0][p], cs + t * kHalf + el) : values_of(kv[1][p]);
+      };
       float top = 0.0f;
-      bool bad = false;
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
-        const int t = tok0 + p * kTokens;
-        if (t >= n) continue;
-        x[p] = load_eight(src + t * ld, kHalf);
-        if (part == 0) rotate(x[p], cs + t * kHalf + 4 * lane8);
+        const Sixteen x = value(p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // a NaN is stored as 0, an infinity as the largest code; both raise the status
-          const float m0 = fabsf(x[p].lo[i]), m1 = fabsf(x[p].hi[i]);
-          if (!(m0 <= 3.4028235e38f)) {
-            bad = true;
-            if (m0 != m0) x[p].lo[i] = 0.0f;
-          } else {
-            top = fmaxf(top, m0);
-          }
-          if (!(m1 <= 3.4028235e38f)) {
-            bad = true;
-            if (m1 != m1) x[p].hi[i] = 0.0f;
-          } else {
-            top = fmaxf(top, m1);
-          }
-        }
+        for (int i = 0; i < 8; ++i) top = max_mag(max_mag(top, x.lo[i]), x.hi[i]);
       }
-      if (bad) raise_status(kStatusNonFinite);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      if ((tid & 31) == 0) warp_max[buf][tid >> 5] = top;
       // older tokens keep at least their exponent
       const int before = lo > page0 ? min(max(static_cast<int>(*scale) - 127, kExpMin), kExpMax) : kExpMin;
-      __syncthreads();
-      top = warp_max[buf][0];
+      top = block_max(top);
+      const bool bad = !(top <= 3.4028235e38f);
+      if (bad) {  // the largest finite magnitude decides; a NaN is stored as 0, an infinity as the largest code
+        if (tid == 0) raise_status(kStatusNonFinite);
+        top = 0.0f;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_max[buf][w]);
-      buf ^= 1;  // the next maximum is written while this one may still be read
+        for (int p = 0; p < PASSES; ++p) {
+          const Sixteen x = value(p);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (fabsf(x.lo[i]) <= 3.4028235e38f) top = fmaxf(top, fabsf(x.lo[i]));
+            if (fabsf(x.hi[i]) <= 3.4028235e38f) top = fmaxf(top, fabsf(x.hi[i]));
+          }
+        }
+        top = block_max(top);
+      }
       const int e = max(exponent_for(top), before);
       uint8_t* dst = pages + (static_cast<int64_t>(physical) * a.n_kv + h) * a.page * D;
       const float inv = pow2f(-e);
@@ -194,11 +244,19 @@ __global__ void __launch_bounds__(THREADS)
       for (int p = 0; p < PASSES; ++p) {
         const int t = tok0 + p * kTokens;
         if (t >= n) continue;
-        uint8_t* o = dst + static_cast<int64_t>(lo - page0 + t) * D + 4 * lane8;
-        *reinterpret_cast<uint32_t*>(o) =
-            e4m3x4(x[p].lo[0] * inv, x[p].lo[1] * inv, x[p].lo[2] * inv, x[p].lo[3] * inv);
-        *reinterpret_cast<uint32_t*>(o + kHalf) =
-            e4m3x4(x[p].hi[0] * inv, x[p].hi[1] * inv, x[p].hi[2] * inv, x[p].hi[3] * inv);
+        Sixteen x = value(p);
+        if (bad) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (x.lo[i] != x.lo[i]) x.lo[i] = 0.0f;
+            if (x.hi[i] != x.hi[i]) x.hi[i] = 0.0f;
+          }
+        }
+        uint8_t* o = dst + static_cast<int64_t>(lo - page0 + t) * D + el;
+        *reinterpret_cast<uint2*>(o) = make_uint2(e4m3x4(x.lo[0] * inv, x.lo[1] * inv, x.lo[2] * inv, x.lo[3] * inv),
+                                                  e4m3x4(x.lo[4] * inv, x.lo[5] * inv, x.lo[6] * inv, x.lo[7] * inv));
+        *reinterpret_cast<uint2*>(o + kHalf) = make_uint2(e4m3x4(x.hi[0] * inv, x.hi[1] * inv, x.hi[2] * inv, x.hi[3] * inv),
+                                                          e4m3x4(x.hi[4] * inv, x.hi[5] * inv, x.hi[6] * inv, x.hi[7] * inv));
       }
       if (lo > page0 && e > before) {
         const float f = before - e < -126 ? 0.0f : pow2f(before - e);
@@ -208,7 +266,7 @@ __global__ void __launch_bounds__(THREADS)
           w[i] = e4m3x4(p0.x * f, p0.y * f, p1.x * f, p1.y * f);
         }
       }
-      // every thread has read the old scale: the barrier lies between
+      // every thread has read the old scale: the maximum's barrier lies between
       if (tid == 0) *scale = static_cast<uint8_t>(e + 127);
     }
   }
@@ -222,7 +280,8 @@ cudaError_t append(const Kv8Args& a, const uint16_t* qkv, const RopeTurns& turns
   const int tokens = a.max_new < a.page ? a.max_new : a.page;
   const int smem = tokens * (D / 2) * 8;
   auto kern = kv8_append_kernel<D, PASSES, THREADS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), 128 * (D / 2) * 8, allowed);
   if (e != cudaSuccess) return e;
   // as many heads to a block as leave four blocks to an SM: they share its cosines and sines
   const int64_t blocks = static_cast<int64_t>(per_seq) * a.S;
@@ -240,13 +299,13 @@ template <int D>
 cudaError_t append_d(const Kv8Args& a, const uint16_t* qkv, const RopeTurns& t, uint8_t* kp, uint8_t* vp, uint8_t* ks,
                      uint8_t* vs, uint16_t* q, cudaStream_t st) {
   // passes x tokens per pass >= the new tokens that a page can take
-  constexpr int kPer128 = 128 / (D / 8), kPer256 = 256 / (D / 8);
+  constexpr int kPer128 = 128 / (D / 16), kPer256 = 256 / (D / 16);
   const int most = a.max_new < a.page ? a.max_new : a.page;
   if (most <= kPer128) return append<D, 1, 128>(a, qkv, t, kp, vp, ks, vs, q, st);
   if (most <= kPer256) return append<D, 1, 256>(a, qkv, t, kp, vp, ks, vs, q, st);
   if (most <= 2 * kPer256) return append<D, 2, 256>(a, qkv, t, kp, vp, ks, vs, q, st);
-  if (most <= 4 * kPer256) return append<D, 4, 256>(a, qkv, t, kp, vp, ks, vs, q, st);
-  return append<D, 8, 256>(a, qkv, t, kp, vp, ks, vs, q, st);
+  if constexpr (D == 128) return append<D, 4, 256>(a, qkv, t, kp, vp, ks, vs, q, st);
+  return cudaErrorInvalidValue;  // not reached: a page has at most 128 tokens
 }
 
 }  // namespace
