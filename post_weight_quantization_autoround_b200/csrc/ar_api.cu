@@ -1226,7 +1226,8 @@ ar_status ar_mxfp4_gemm(const uint16_t* A, int64_t T, const uint8_t* codes, cons
     if (e != cudaSuccess) return cuda_fail(e, "expand_mxfp4 launch");
     e = launch_gemm_store_bf16(A, W, out, Ti, Ni, Ki, s);
   } else {
-    e = launch_mxfp4_tc(A, Ti, codes, scales, Ni, Ki, out, s);
+    e = T <= 8 ? launch_mxfp4_dec(A, Ti, codes, scales, Ni, Ki, out, s) : cudaErrorNotSupported;
+    if (e == cudaErrorNotSupported) e = launch_mxfp4_tc(A, Ti, codes, scales, Ni, Ki, out, s);
   }
   if (e != cudaSuccess) return cuda_fail(e, "mxfp4 gemm launch");
   return end_call();
