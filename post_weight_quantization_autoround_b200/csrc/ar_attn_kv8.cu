@@ -29,8 +29,6 @@
 //    and a captured graph keeps working as they grow).  A row tile split between blocks is
 //    joined by a second kernel from unnormalised sums in the workspace, in block order: no
 //    atomics, the same result every time.
-#include <cuda_fp8.h>
-
 #include "ar_internal.h"
 
 namespace ar {
@@ -103,14 +101,17 @@ __device__ __forceinline__ int row_tiles(const Seq& q, int rows, int group) {
   return (q.n_new * group + rows - 1) / rows;
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// the 4 codes of a word, two to a register, in order
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -118,7 +119,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
@@ -379,8 +380,9 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D, NT>::kBlocksPerSm)
           const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
-            const uint32_t a0 = e4m3x2_f16(w0[i4] & 0xFFFFu), a2 = e4m3x2_f16(w0[i4] >> 16);
-            const uint32_t a1 = e4m3x2_f16(w1[i4] & 0xFFFFu), a3 = e4m3x2_f16(w1[i4] >> 16);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_f16(w0[i4], a0, a2);
+            e4m3x4_f16(w1[i4], a1, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16(z[nt], a0, a1, a2, a3, qf[nt][4 * v + i4][0], qf[nt][4 * v + i4][1]);
           }
@@ -445,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D, NT>::kBlocksPerSm)
           ldmatrix_x4_trans(r, va + swz<D>(8 * ((lane >> 3) & 1) + (lane & 7), mt + (lane >> 4)));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t lo = __byte_perm(r[2 * h], 0u, 0x3120), hi = __byte_perm(r[2 * h + 1], 0u, 0x3120);
-            const uint32_t a0 = e4m3x2_f16(lo & 0xFFFFu), a1 = e4m3x2_f16(lo >> 16);
-            const uint32_t a2 = e4m3x2_f16(hi & 0xFFFFu), a3 = e4m3x2_f16(hi >> 16);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_f16(__byte_perm(r[2 * h], 0u, 0x3120), a0, a1);
+            e4m3x4_f16(__byte_perm(r[2 * h + 1], 0u, 0x3120), a2, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16(o[mt + h][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
           }

@@ -25,8 +25,6 @@
 // every load of a thread's two chunks is issued before the first is used.
 // Measured (8192 x 28672, V and alpha given, W_hat, codes and scales written, 8.66
 // bytes a weight): see the launch functions.
-#include <cuda_fp4.h>
-
 #include "ar_internal.h"
 
 namespace ar {
@@ -90,11 +88,14 @@ __device__ __forceinline__ void mx_unpack(const uint4& w, float (&x)[8]) {
 
 // two values -> E2M1 pair (low nibble a) and back to floats
 __device__ __forceinline__ uint32_t e2m1_pair(float a, float b) {
-  return __nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest);
+  uint32_t r;
+  asm("{\n\t.reg .b8 q;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %2, %1;\n\tcvt.u32.u8 %0, q;\n\t}" : "=r"(r) : "f"(a), "f"(b));
+  return r;
 }
 __device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
-  return __half22float2(__half2(h));
+  uint32_t h;
+  asm("{\n\t.reg .b8 q;\n\tcvt.u8.u32 q, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, q;\n\t}" : "=r"(h) : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 __global__ void __launch_bounds__(kMxThreads) qdq_mxfp4_kernel(const uint16_t* __restrict__ W,

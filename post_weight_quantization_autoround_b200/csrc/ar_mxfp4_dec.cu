@@ -18,8 +18,6 @@
 //    part in a slot of its own.  The CTAs of a cluster split k, so that a block's share of
 //    the activations stays in shared memory; their sums meet through distributed shared
 //    memory.  Parts are added in a fixed order.
-#include <cuda_fp4.h>
-
 #include "ar_internal.h"
 
 namespace ar {
@@ -53,9 +51,13 @@ struct DecParams {
   int wide;        // a row's scale bytes of a span are one aligned 8-byte word
 };
 
-__device__ __forceinline__ uint32_t e2m1x2_f16(uint32_t byte) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// the 8 codes of a word, two to a register, in order
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
 
 __device__ __forceinline__ uint32_t e8m0x2_bf16(uint32_t two) {
@@ -66,7 +68,7 @@ __device__ __forceinline__ uint32_t e8m0x2_bf16(uint32_t two) {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1, const float (&c)[4]) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
@@ -232,10 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
         const uint32_t x0 = lds32(w + off), x1 = lds32(w + off + 1024);
         const uint4 a = lds128(ab + b * p.T * 64);
         float d[4];
-        mma_f16(d, e2m1x2_f16(x0 & 0xFFu), e2m1x2_f16(x1 & 0xFFu), e2m1x2_f16((x0 >> 8) & 0xFFu),
-                e2m1x2_f16((x1 >> 8) & 0xFFu), a.x, a.y, zero);
-        mma_f16(d, e2m1x2_f16((x0 >> 16) & 0xFFu), e2m1x2_f16((x1 >> 16) & 0xFFu), e2m1x2_f16(x0 >> 24),
-                e2m1x2_f16(x1 >> 24), a.z, a.w, d);
+        uint32_t h0[4], h1[4];
+        e2m1x8_f16(x0, h0);
+        e2m1x8_f16(x1, h1);
+        mma_f16(d, h0[0], h1[0], h0[1], h1[1], a.x, a.y, zero);
+        mma_f16(d, h0[2], h1[2], h0[3], h1[3], a.z, a.w, d);
         if ((b & 1) == 0) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) bf[h] = e8m0x2_bf16((b < 4 ? sc[h].x : sc[h].y) >> (8 * (b & 2)));
