@@ -20,11 +20,12 @@
 //  * S^T leaves the tensor core with tokens along lanes' rows; movmatrix transposes the
 //    8 x 8 blocks into the B operand of O^T.  V^T comes from ldmatrix.trans on byte pairs:
 //    one byte permute separates even and odd dimensions.
-//  * Each of a block's 8 warps streams its own 16-token tiles (2 KB of keys and of values
+//  * Each of a block's warps streams its own tiles of 32 tokens (4 KB of keys and of values
 //    at d = 128; TMA boxes with the hardware swizzle, so neither read conflicts)
-//    through a private ring; nothing but the end of an item synchronises the block.  Two
-//    blocks share an SM up to 8 rows, so that one streams while the other joins.
-//  * The work is the list of (sequence, row tile, head, 128 tokens) units.  Every block takes
+//    through a private ring; nothing but the end of an item synchronises the block, and the
+//    copies run on into the next item meanwhile (its pages and scales are looked up an
+//    item ahead).  Two blocks of 6 warps share an SM up to 8 rows.
+//  * The work is the list of (sequence, row tile, head, 192 or 256 tokens) units.  Every block takes
 //    an equal run of it, found from the lengths on the device (the host does not know them,
 //    and a captured graph keeps working as they grow).  A row tile split between blocks is
 //    joined by a second kernel from unnormalised sums in the workspace, in block order: no
@@ -34,17 +35,21 @@
 namespace ar {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;               // tokens of a warp's step
-constexpr int kUnit = kWarps * kTile;   // tokens of a work unit
-constexpr int kChunk = 32;              // steps whose pages and scales the lanes hold
+constexpr int kBox = 16;       // tokens of a copy: a page is a multiple of it
+constexpr int kChunk = 32;     // steps whose pages and scales the lanes hold
+constexpr int kMaxWarps = 8;
 
 template <int D, int NT>
 struct AttnCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kBlocksPerSm = NT == 1 ? 2 : 1;
-  static constexpr int kStages = NT == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 4 : 6);
+  static constexpr int kWarps = NT == 1 ? 6 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kHalves = NT == 4 ? 1 : 2;     // boxes of 16 tokens in a warp's step
+  static constexpr int kTile = kBox * kHalves;        // tokens of a step
+  static constexpr int kUnit = kWarps * kTile;        // tokens of a work unit
+  static constexpr int kStages = D == 128 ? (NT == 4 ? 4 : 2) : 4;
+  static constexpr int kBoxBytes = kBox * D;
   static constexpr int kTileBytes = kTile * D;        // of keys, and of values
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
@@ -55,8 +60,9 @@ struct AttnCfg {
 };
 
 struct AttnCtl {
-  uint64_t full[kWarps][8];
-  float m[kWarps][32], l[kWarps][32];  // per warp and row
+  uint64_t full[kMaxWarps][4];
+  float m[kMaxWarps][32], l[kMaxWarps][32];  // per warp and row
+  float row_l[32];                           // of the block: 1 / row sum
   int abort_flag;
 };
 
@@ -95,7 +101,10 @@ __device__ __forceinline__ int tile_keys(const Seq& q, int rt, int rows, int gro
   return max(0, q.len - q.n_new + last + 1);
 }
 
-__device__ __forceinline__ int units_of(int keys) { return keys <= kUnit ? 1 : (keys + kUnit - 1) / kUnit; }
+template <int UNIT>
+__device__ __forceinline__ int units_of(int keys) {
+  return keys <= UNIT ? 1 : (keys + UNIT - 1) / UNIT;
+}
 
 __device__ __forceinline__ int row_tiles(const Seq& q, int rows, int group) {
   return (q.n_new * group + rows - 1) / rows;
@@ -154,11 +163,29 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {
   return static_cast<uint32_t>(row * D + ((D == 128 ? (chunk ^ (row & 7)) : (chunk ^ ((row >> 1) & 3))) << 4));
 }
 
+// where a block's run of units stands
+struct Pos {
+  int s, rt, head;   // sequence, row tile, key/value head
+  Seq seq;
+  int item_units;    // units of the row tile (for each head)
+  uint32_t item0;    // first unit of the row tile's first head
+  uint32_t at;       // next unit
+};
+
+// the steps of one warp in up to kChunk units of an item, one a lane
+struct Steps {
+  int row[2];      // first row of the step's boxes in the cache, -1: nothing to read
+  uint32_t exps;   // scale codes: key, value of the first box, key, value of the second
+  uint32_t use, issue;  // steps still to be computed, still to be copied
+  int units;
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, AttnCfg<D, NT>::kBlocksPerSm)
+__global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlocksPerSm)
     attn_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using Cfg = AttnCfg<D, NT>;
-  constexpr int kRows = Cfg::kRows;
+  constexpr int kRows = Cfg::kRows, kWarps = Cfg::kWarps, kThreads = Cfg::kThreads, kHalves = Cfg::kHalves;
+  constexpr int kTile = Cfg::kTile, kUnit = Cfg::kUnit;
   constexpr int kKs = D / 16;      // k-steps of S^T
   constexpr int kMt = D / 16;      // 16-dimension tiles of O^T
   constexpr int kQr = D / 64;      // 16-byte loads of a K row per lane
@@ -181,15 +208,24 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D, NT>::kBlocksPerSm)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  // units of every sequence, a warp each
-  for (int s = warp; s < a.S; s += kWarps) {
-    const Seq q = load_seq(a, s);
-    const int nrt = row_tiles(q, kRows, group);
-    uint32_t u = 0;
-    for (int rt = lane; rt < nrt; rt += 32) u += units_of(tile_keys(q, rt, kRows, group));
+  // units of every sequence: a thread each where it is one row tile, else a warp each
+  if (a.max_new * group <= kRows) {
+    for (int s = threadIdx.x; s < a.S; s += kThreads) {
+      const Seq q = load_seq(a, s);
+      uint32_t u = 0;
+      for (int rt = 0; rt < row_tiles(q, kRows, group); ++rt) u += units_of<kUnit>(tile_keys(q, rt, kRows, group));
+      prefix[s + 1] = u * a.n_kv;
+    }
+  } else {
+    for (int s = warp; s < a.S; s += kWarps) {
+      const Seq q = load_seq(a, s);
+      const int nrt = row_tiles(q, kRows, group);
+      uint32_t u = 0;
+      for (int rt = lane; rt < nrt; rt += 32) u += units_of<kUnit>(tile_keys(q, rt, kRows, group));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-    if (lane == 0) prefix[s + 1] = u * a.n_kv;
+      for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+      if (lane == 0) prefix[s + 1] = u * a.n_kv;
+    }
   }
   __syncthreads();
   if (warp == 0) {
@@ -213,8 +249,8 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D, NT>::kBlocksPerSm)
   if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (u_begin >= u_end) return;
 
-  // where the run starts: sequence, row tile, head, unit
-  int s;
+  // where the run starts
+  Pos cur;
   {
     int lo = 0, hi = a.S - 1;
     while (lo < hi) {
@@ -222,161 +258,209 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D, NT>::kBlocksPerSm)
       if (prefix[mid + 1] > u_begin) hi = mid;
       else lo = mid + 1;
     }
-    s = lo;
+    cur.s = lo;
+    cur.seq = load_seq(a, lo);
+    cur.at = u_begin;
+    cur.item0 = prefix[lo];
+    for (cur.rt = 0;; ++cur.rt) {
+      cur.item_units = units_of<kUnit>(tile_keys(cur.seq, cur.rt, kRows, group));
+      const uint32_t next = cur.item0 + static_cast<uint32_t>(cur.item_units) * a.n_kv;
+      if (next > cur.at) break;
+      cur.item0 = next;
+    }
+    cur.head = static_cast<int>((cur.at - cur.item0) / cur.item_units);
   }
-  Seq seq = load_seq(a, s);
-  int rt = 0, head, item_units;
-  uint32_t at = u_begin, item0 = prefix[s];  // item0: first unit of the current row tile's heads
-  for (;; ++rt) {
-    item_units = units_of(tile_keys(seq, rt, kRows, group));
-    const uint32_t next = item0 + static_cast<uint32_t>(item_units) * a.n_kv;
-    if (next > at) break;
-    item0 = next;
-  }
-  head = static_cast<int>((at - item0) / item_units);
-
-  uint32_t stage = 0, phase = 0;
-  bool alive = true;
-
-  while (at < u_end) {
-    const uint32_t first_unit = item0 + static_cast<uint32_t>(head) * item_units;
-    const int t0 = static_cast<int>(at - first_unit);                                  // units of the item done before
-    const int t1 = static_cast<int>(min(u_end - first_unit, static_cast<uint32_t>(item_units)));  // and after this segment
-    const int keys = tile_keys(seq, rt, kRows, group);
-    const int start = seq.len - seq.n_new;
-    const int row0 = rt * kRows;
-    const int n_rows = seq.n_new * group;
-
-    // ---- queries: B operand registers, normalised; a row's factor to log2 units
-    uint32_t qf[NT][kKs][2];
-    float fac[NT][2];
-    int lim[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + nt * 8 + g;
-      uint32_t raw[D / 8];  // this lane's D / 4 values (dimensions D / 4 c ..), bf16 pairs
-      if (r < n_rows) {
-        const int tok = r / group, qh = head * group + (r - tok * group);
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (static_cast<int64_t>(seq.first + tok) * a.n_heads + qh) * D + c * (D / 4));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 v = __ldg(src + i);
-          raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+  auto first_unit = [&](const Pos& q) { return q.item0 + static_cast<uint32_t>(q.head) * q.item_units; };
+  auto advance = [&](Pos& q, int units) {  // false at the end of the block's run
+    q.at += units;
+    if (q.at >= u_end) return false;
+    if (q.at == first_unit(q) + q.item_units) {
+      if (++q.head == a.n_kv) {
+        q.head = 0;
+        q.item0 = q.at;
+        if (++q.rt >= row_tiles(q.seq, kRows, group)) {
+          q.rt = 0;
+          do {
+            q.seq = load_seq(a, ++q.s);
+          } while (q.seq.n_new == 0 && q.s + 1 < a.S);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) raw[i] = 0u;
-      }
-      uint32_t mag = 0;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) mag = __vmaxu2(mag, raw[i] & 0x7FFF7FFFu);
-      mag = max(mag & 0xFFFFu, mag >> 16);
-      mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
-      mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
-      // 2^qe q lies below 2^14; qe is kept where both powers are normal
-      const int qe = min(126, max(-120, 13 + 127 - static_cast<int>(mag >> 7)));
-      const float up = __uint_as_float(static_cast<uint32_t>(qe + 127) << 23);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
-#pragma unroll
-      for (int i = 0; i < kKs; ++i) {
-        qf[nt][i][0] = pack_f16x2(bf16_lo(raw[2 * i]) * up, bf16_hi(raw[2 * i]) * up);
-        qf[nt][i][1] = pack_f16x2(bf16_lo(raw[2 * i + 1]) * up, bf16_hi(raw[2 * i + 1]) * up);
-      }
-      const float f = down * p.scale_log2;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        fac[nt][j] = __shfl_sync(0xFFFFFFFFu, f, (2 * c + j) * 4);
-        const int rr = row0 + nt * 8 + 2 * c + j;
-        lim[nt][j] = rr < n_rows ? start + rr / group + 1 : 0;  // keys the row sees
+        q.item_units = units_of<kUnit>(tile_keys(q.seq, q.rt, kRows, group));
       }
     }
-
-    float o[kMt][NT][4];
-    float m[NT][2], l[NT][2];
+    return true;
+  };
+  // the next steps at q: lane i looks up pages and scales of unit i
+  auto plan = [&](const Pos& q) {
+    Steps f;
+    const uint32_t fu = first_unit(q);
+    const int unit0 = static_cast<int>(q.at - fu);
+    f.units = static_cast<int>(min(min(u_end, fu + q.item_units) - q.at, static_cast<uint32_t>(kChunk)));
+    const int keys = tile_keys(q.seq, q.rt, kRows, group);
+    f.exps = 0u;
+    f.row[0] = f.row[1] = -1;
 #pragma unroll
-    for (int i = 0; i < kMt; ++i)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        m[nt][j] = -INFINITY;
-        l[nt][j] = 0.f;
+    for (int h = 0; h < kHalves; ++h) {
+      const int t = (unit0 + lane) * kUnit + warp * kTile + h * kBox;
+      if (lane < f.units && t < keys) {
+        const int pg = __ldg(a.table + static_cast<int64_t>(q.s) * a.max_pages + t / a.page);
+        if (pg >= 0 && pg < a.n_pages) {
+          const int64_t ph = static_cast<int64_t>(pg) * a.n_kv + q.head;
+          f.row[h] = static_cast<int>(ph * a.page + t % a.page);
+          f.exps |= (static_cast<uint32_t>(__ldg(p.ks + ph)) | (static_cast<uint32_t>(__ldg(p.vs + ph)) << 8)) << (16 * h);
+        } else {
+          raise_status(kStatusBadIndex);
+        }
       }
-    const int full_below = start + row0 / group + 1;  // tokens before this are seen by every row of the tile
+    }
+    f.use = f.issue = __ballot_sync(0xFFFFFFFFu, f.row[0] >= 0 || f.row[1] >= 0);
+    return f;
+  };
 
-    // ---- the segment's tokens, kChunk steps at a time
-    for (int cu = t0; alive && cu < t1; cu += kChunk) {
-      const int steps_max = min(kChunk, t1 - cu);
-      // lane i: page, place and exponents of step i
-      int row_of = -1, ek = 0, ev = 0;
-      {
-        const int t = (cu + lane) * kUnit + warp * kTile;
-        if (lane < steps_max && t < keys) {
-          const int pg = __ldg(a.table + static_cast<int64_t>(s) * a.max_pages + t / a.page);
-          if (pg >= 0 && pg < a.n_pages) {
-            const int64_t ph = static_cast<int64_t>(pg) * a.n_kv + head;
-            row_of = static_cast<int>(ph * a.page + t % a.page);
-            ek = static_cast<int>(__ldg(p.ks + ph)) - 127;
-            ev = static_cast<int>(__ldg(p.vs + ph)) - 127;
-          } else {
-            raise_status(kStatusBadIndex);
+  uint32_t stage = 0, phase = 0, ahead = 0;  // next slot to read, its phase, next slot to fill
+  int inflight = 0;
+  bool alive = true;
+  auto issue = [&](Steps& f) {
+    const int i = __ffs(f.issue) - 1;
+    f.issue &= f.issue - 1;
+    int r[2] = {__shfl_sync(0xFFFFFFFFu, f.row[0], i), -1};
+    if (kHalves == 2) r[1] = __shfl_sync(0xFFFFFFFFu, f.row[1], i);
+    if (lane == 0) {
+      uint8_t* dst = ring + ahead * Cfg::kStageBytes;
+      uint64_t* bar = &ctl->full[warp][ahead];
+      mbar_arrive_expect_tx(bar, (r[0] >= 0 ? 2 * Cfg::kBoxBytes : 0) + (r[1] >= 0 ? 2 * Cfg::kBoxBytes : 0));
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        if (r[h] >= 0) {
+          tma_load_2d(dst + h * Cfg::kBoxBytes, &tmK, bar, 0, r[h]);
+          tma_load_2d(dst + Cfg::kTileBytes + h * Cfg::kBoxBytes, &tmV, bar, 0, r[h]);
+        }
+    }
+    ahead = ahead + 1 == Cfg::kStages ? 0 : ahead + 1;
+    ++inflight;
+  };
+
+  Steps fc = plan(cur);
+  Pos nxt = cur;
+  bool more = advance(nxt, fc.units);
+  Steps fn;
+  if (more) fn = plan(nxt);
+  else fn.use = fn.issue = 0u;
+  // Copies run ahead into the next steps planned, past the end of an item.  Called wherever a slot or new steps
+  // come free: after a step, and after planning (a warp may have had nothing to do in two plans running).
+  auto refill = [&]() {
+    while (alive && inflight < Cfg::kStages && (fc.issue | fn.issue)) {
+      if (fc.issue) issue(fc);
+      else issue(fn);
+    }
+  };
+
+  uint32_t qf[NT][kKs][2];
+  float fac[NT][2];
+  int lim[NT][2];
+  float o[kMt][NT][4];
+  float m[NT][2], l[NT][2];
+  int t_first = 0, full_below = 0, keys = 0;  // of the segment: its first unit in the item, tokens every row sees, keys
+  bool fresh = true;
+
+  for (;;) {
+    refill();
+    const int row0 = cur.rt * kRows;
+    const int n_rows = cur.seq.n_new * group;
+    if (fresh) {
+      // ---- a new item: queries as B operand registers, normalised; a row's factor to log2 units
+      const int start = cur.seq.len - cur.seq.n_new;
+      t_first = static_cast<int>(cur.at - first_unit(cur));
+      keys = tile_keys(cur.seq, cur.rt, kRows, group);
+      full_below = start + row0 / group + 1;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = row0 + nt * 8 + g;
+        uint32_t raw[D / 8];  // this lane's D / 4 values (dimensions D / 4 c ..), bf16 pairs
+        if (r < n_rows) {
+          const int tok = r / group, qh = cur.head * group + (r - tok * group);
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + (static_cast<int64_t>(cur.seq.first + tok) * a.n_heads + qh) * D + c * (D / 4));
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const uint4 v = __ldg(src + i);
+            raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) raw[i] = 0u;
+        }
+        uint32_t mag = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) mag = __vmaxu2(mag, raw[i] & 0x7FFF7FFFu);
+        mag = max(mag & 0xFFFFu, mag >> 16);
+        mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
+        mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
+        // 2^qe q lies below 2^14; qe is kept where both powers are normal
+        const int qe = min(126, max(-120, 13 + 127 - static_cast<int>(mag >> 7)));
+        const float up = __uint_as_float(static_cast<uint32_t>(qe + 127) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
+#pragma unroll
+        for (int i = 0; i < kKs; ++i) {
+          qf[nt][i][0] = pack_f16x2(bf16_lo(raw[2 * i]) * up, bf16_hi(raw[2 * i]) * up);
+          qf[nt][i][1] = pack_f16x2(bf16_lo(raw[2 * i + 1]) * up, bf16_hi(raw[2 * i + 1]) * up);
+        }
+        const float f = down * p.scale_log2;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          fac[nt][j] = __shfl_sync(0xFFFFFFFFu, f, (2 * c + j) * 4);
+          const int rr = row0 + nt * 8 + 2 * c + j;
+          lim[nt][j] = rr < n_rows ? start + rr / group + 1 : 0;  // keys the row sees
+          m[nt][j] = -INFINITY;
+          l[nt][j] = 0.f;
         }
       }
-      const uint32_t have = __ballot_sync(0xFFFFFFFFu, row_of >= 0);  // steps with something to read
-      uint32_t to_issue = have, to_use = have;
-      auto issue = [&](uint32_t st) {
-        const int i = __ffs(to_issue) - 1;
-        to_issue &= to_issue - 1;
-        const int r = __shfl_sync(0xFFFFFFFFu, row_of, i);
-        if (lane == 0) {
-          uint8_t* dst = ring + st * Cfg::kStageBytes;
-          mbar_arrive_expect_tx(&ctl->full[warp][st], Cfg::kStageBytes);
-          tma_load_2d(dst, &tmK, &ctl->full[warp][st], 0, r);
-          tma_load_2d(dst + Cfg::kTileBytes, &tmV, &ctl->full[warp][st], 0, r);
-        }
-      };
-      uint32_t ahead = stage;
-      for (int i = 0; i < Cfg::kStages && to_issue; ++i) {
-        issue(ahead);
-        ahead = ahead + 1 == Cfg::kStages ? 0 : ahead + 1;
-      }
-      while (to_use) {
-        const int i = __ffs(to_use) - 1;
-        to_use &= to_use - 1;
-        const int ekb = __shfl_sync(0xFFFFFFFFu, ek, i), evb = __shfl_sync(0xFFFFFFFFu, ev, i);
-        const int tb = (cu + i) * kUnit + warp * kTile;  // first token of the step
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[warp][stage], phase, &ctl->abort_flag))) {
-          alive = false;
-          break;
-        }
-        uint8_t* kt = ring + stage * Cfg::kStageBytes;
-        const uint32_t ka = smem_u32(kt), va = ka + Cfg::kTileBytes;
-        if (tb + kTile > seq.len) {
-          // rows past the sequence's end hold anything, a NaN too: their values become zeros
-          // (their scores are masked below)
-          for (int e = lane; e < kTile * (D / 16); e += 32) {
-            const int r = e / (D / 16);
-            if (tb + r >= seq.len) *reinterpret_cast<uint4*>(kt + Cfg::kTileBytes + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          __syncwarp();
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the slot is copied into again
-        }
-
-        // ---- S^T: tokens g, g + 8 of the tile; this lane's codes are dimensions D / 4 c ..
-        float z[NT][4];
+#pragma unroll
+      for (int i = 0; i < kMt; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) z[nt][j] = 0.f;
+          for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.f;
+    }
+
+    const int unit0 = static_cast<int>(cur.at - first_unit(cur));
+    while (alive && fc.use) {
+      const int i = __ffs(fc.use) - 1;
+      fc.use &= fc.use - 1;
+      const uint32_t exps = __shfl_sync(0xFFFFFFFFu, fc.exps, i);
+      const int tb = (unit0 + i) * kUnit + warp * kTile;  // first token of the step
+      // a step whose boxes are not both there: past the keys, or a page that is not in the pool
+      const uint32_t have = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, (fc.row[0] >= 0 ? 1 : 0) | (fc.row[1] >= 0 ? 2 : 0), i));
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[warp][stage], phase, &ctl->abort_flag))) {
+        alive = false;
+        break;
+      }
+      uint8_t* kt = ring + stage * Cfg::kStageBytes;
+      const uint32_t ka = smem_u32(kt), va = ka + Cfg::kTileBytes;
+      const bool whole_boxes = have == (kHalves == 2 ? 3u : 1u);
+      if (tb + kTile > keys || !whole_boxes) {
+        // rows past the keys, or of a box that was not copied, hold anything, a NaN too: their values
+        // become zeros (their scores are masked below)
+        for (int e = lane; e < kTile * (D / 16); e += 32) {
+          const int r = e / (D / 16);
+          if (tb + r >= keys || !((have >> (r / kBox)) & 1u))
+            *reinterpret_cast<uint4*>(kt + Cfg::kTileBytes + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the slot is copied into again
+      }
+
+      // ---- S^T: tokens g, g + 8 of each box; this lane's codes are dimensions D / 4 c ..
+      float z[NT][kHalves][4];
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[nt][h][j] = 0.f;
 #pragma unroll
         for (int v = 0; v < kQr; ++v) {
-          const uint4 x0 = lds128(ka + swz<D>(g, kQr * c + v)), x1 = lds128(ka + swz<D>(g + 8, kQr * c + v));
+          const uint4 x0 = lds128(ka + swz<D>(h * kBox + g, kQr * c + v));
+          const uint4 x1 = lds128(ka + swz<D>(h * kBox + g + 8, kQr * c + v));
           const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
@@ -384,191 +468,199 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D, NT>::kBlocksPerSm)
             e4m3x4_f16(w0[i4], a0, a2);
             e4m3x4_f16(w1[i4], a1, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(z[nt], a0, a1, a2, a3, qf[nt][4 * v + i4][0], qf[nt][4 * v + i4][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(z[nt][h], a0, a1, a2, a3, qf[nt][4 * v + i4][0], qf[nt][4 * v + i4][1]);
           }
         }
+      }
 
-        // ---- softmax: u = z log2(e) sm_scale 2^ek + ev
-        const float fk = __uint_as_float(static_cast<uint32_t>(min(max(ekb, -126), 127) + 127) << 23);
-        const float fe = static_cast<float>(evb);
-        const float back = __uint_as_float(static_cast<uint32_t>(min(max(-evb, -126), 127) + 127) << 23);  // 2^-ev
-        const bool masked = tb + kTile > full_below;
-        uint32_t pb[NT][2];
+      // ---- softmax: u = z log2(e) sm_scale 2^ek + ev
+      float fk[kHalves], fe[kHalves], back[kHalves];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float top[2];
+      for (int h = 0; h < kHalves; ++h) {
+        const uint32_t ek = (exps >> (16 * h)) & 0xFFu, ev = (exps >> (16 * h + 8)) & 0xFFu;
+        fk[h] = __uint_as_float(max(min(ek, 254u), 1u) << 23);
+        fe[h] = static_cast<float>(static_cast<int>(ev) - 127);
+        back[h] = __uint_as_float(max(254u - min(ev, 253u), 1u) << 23);  // 2^-ev
+      }
+      const bool masked = tb + kTile > full_below || !whole_boxes;
+      uint32_t pb[NT][kHalves][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float top[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          top[j] = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            const float f = fac[nt][j] * fk[h];
+            z[nt][h][j] = fmaf(z[nt][h][j], f, fe[h]);
+            z[nt][h][2 + j] = fmaf(z[nt][h][2 + j], f, fe[h]);
+            if (masked) {
+              const int end = ((have >> h) & 1u) ? lim[nt][j] : 0;
+              if (tb + h * kBox + g >= end) z[nt][h][j] = -INFINITY;
+              if (tb + h * kBox + g + 8 >= end) z[nt][h][2 + j] = -INFINITY;
+            }
+            top[j] = fmaxf(top[j], fmaxf(z[nt][h][j], z[nt][h][2 + j]));
+          }
+          top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 4));
+          top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 8));
+          top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 16));
+        }
+        if (__any_sync(0xFFFFFFFFu, top[0] > m[nt][0] || top[1] > m[nt][1])) {
+          float sc[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float f = fac[nt][j] * fk;
-            z[nt][j] = fmaf(z[nt][j], f, fe);
-            z[nt][2 + j] = fmaf(z[nt][2 + j], f, fe);
-            if (masked) {
-              if (tb + g >= lim[nt][j]) z[nt][j] = -INFINITY;
-              if (tb + g + 8 >= lim[nt][j]) z[nt][2 + j] = -INFINITY;
-            }
-            top[j] = fmaxf(z[nt][j], z[nt][2 + j]);
-            top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 4));
-            top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 8));
-            top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 16));
+            const float mn = fmaxf(m[nt][j], top[j]);
+            sc[j] = mn == -INFINITY ? 1.0f : ex2(m[nt][j] - mn);
+            m[nt][j] = mn;
+            l[nt][j] *= sc[j];
           }
-          if (__any_sync(0xFFFFFFFFu, top[0] > m[nt][0] || top[1] > m[nt][1])) {
-            float sc[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float mn = fmaxf(m[nt][j], top[j]);
-              sc[j] = mn == -INFINITY ? 1.0f : ex2(m[nt][j] - mn);
-              m[nt][j] = mn;
-              l[nt][j] *= sc[j];
-            }
-#pragma unroll
-            for (int mt = 0; mt < kMt; ++mt) {
-              o[mt][nt][0] *= sc[0];
-              o[mt][nt][1] *= sc[1];
-              o[mt][nt][2] *= sc[0];
-              o[mt][nt][3] *= sc[1];
-            }
+          for (int mt = 0; mt < kMt; ++mt) {
+            o[mt][nt][0] *= sc[0];
+            o[mt][nt][1] *= sc[1];
+            o[mt][nt][2] *= sc[0];
+            o[mt][nt][3] *= sc[1];
           }
+        }
+        const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
           float pr[4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float base = m[nt][j] == -INFINITY ? 0.0f : m[nt][j];  // no key yet: 2^(-inf) = 0
-            pr[j] = ex2(z[nt][j] - base);
-            pr[2 + j] = ex2(z[nt][2 + j] - base);
-            l[nt][j] = fmaf(pr[j] + pr[2 + j], back, l[nt][j]);
+          for (int j = 0; j < 2; ++j) {  // no key yet: 2^(-inf) = 0
+            pr[j] = ex2(z[nt][h][j] - base[j]);
+            pr[2 + j] = ex2(z[nt][h][2 + j] - base[j]);
+            l[nt][j] = fmaf(pr[j] + pr[2 + j], back[h], l[nt][j]);
           }
-          pb[nt][0] = movmatrix(pack_f16x2(pr[0], pr[1]));
-          pb[nt][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
+          pb[nt][h][0] = movmatrix(pack_f16x2(pr[0], pr[1]));
+          pb[nt][h][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
         }
+      }
 
-        // ---- O^T += V^T P^T, 16 dimensions (one 16-byte chunk of the rows) at a time
+      // ---- O^T += V^T P^T, 16 dimensions (one 16-byte chunk of the rows) at a time
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
 #pragma unroll
         for (int mt = 0; mt < kMt; mt += 2) {
           uint32_t r[4];
-          ldmatrix_x4_trans(r, va + swz<D>(8 * ((lane >> 3) & 1) + (lane & 7), mt + (lane >> 4)));
+          ldmatrix_x4_trans(r, va + swz<D>(h * kBox + 8 * ((lane >> 3) & 1) + (lane & 7), mt + (lane >> 4)));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int x = 0; x < 2; ++x) {
             uint32_t a0, a1, a2, a3;
-            e4m3x4_f16(__byte_perm(r[2 * h], 0u, 0x3120), a0, a1);
-            e4m3x4_f16(__byte_perm(r[2 * h + 1], 0u, 0x3120), a2, a3);
+            e4m3x4_f16(__byte_perm(r[2 * x], 0u, 0x3120), a0, a1);
+            e4m3x4_f16(__byte_perm(r[2 * x + 1], 0u, 0x3120), a2, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(o[mt + h][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[mt + x][nt], a0, a1, a2, a3, pb[nt][h][0], pb[nt][h][1]);
           }
         }
-        __syncwarp();  // the slot has been read
-        if (to_issue) issue(stage);
-        if (++stage == Cfg::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      __syncwarp();  // the slot has been read
+      --inflight;
+      if (++stage == Cfg::kStages) {
+        stage = 0;
+        phase ^= 1u;
       }
-      if (!alive) {
-        // a wait gave up: copies in flight (this step's and those issued ahead) land before the block may end
-        uint32_t st = stage, ph = phase;
-        for (int left = __popc(to_use) + 1 - __popc(to_issue); left > 0; --left) {
-          mbar_wait_drain(&ctl->full[warp][st], ph);
-          if (++st == Cfg::kStages) {
-            st = 0;
-            ph ^= 1u;
-          }
-        }
-        break;
-      }
+      refill();
     }
 
-    // ---- join the warps: maximum and sum of every row, then the sums of 32 dimensions a round
+    const uint32_t fu = first_unit(cur);
+    const int t_end = static_cast<int>(cur.at - fu) + fc.units;  // units of the item done so far
+    const bool segment_ends = fu + t_end == u_end || t_end == cur.item_units;
+    if (segment_ends) {
+      // ---- join the warps: maximum and sum of every row, then the sums of 32 dimensions a round
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], x);
-        if (g == 0) {
-          ctl->m[warp][nt * 8 + 2 * c + j] = m[nt][j];
-          ctl->l[warp][nt * 8 + 2 * c + j] = l[nt][j];
+          for (int x = 4; x < 32; x <<= 1) l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], x);
+          if (g == 0) {
+            ctl->m[warp][nt * 8 + 2 * c + j] = m[nt][j];
+            ctl->l[warp][nt * 8 + 2 * c + j] = l[nt][j];
+          }
         }
-      }
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == item_units;
-    float* slot = p.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * Cfg::kSlotFloats;
-    float wf[NT][2];  // this warp's factor to the block's maximum
+      __syncthreads();
+      const bool whole = t_first == 0 && t_end == cur.item_units;
+      float* slot = p.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (t_first == 0 ? 1 : 0)) * Cfg::kSlotFloats;
+      float wf[NT][2];  // this warp's factor to the block's maximum
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float mx = -INFINITY;
+        for (int j = 0; j < 2; ++j) {
+          float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ctl->m[w][nt * 8 + 2 * c + j]);
-        wf[nt][j] = m[nt][j] == -INFINITY ? 0.0f : ex2(m[nt][j] - mx);
-      }
-    constexpr int kPer = kRows * Cfg::kJoinDims / kThreads > 0 ? kRows * Cfg::kJoinDims / kThreads : 1;
-    // the row sum and maximum that this thread's outputs need (its rows are the same each round)
-    float inv[kPer];
+          for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ctl->m[w][nt * 8 + 2 * c + j]);
+          wf[nt][j] = m[nt][j] == -INFINITY ? 0.0f : ex2(m[nt][j] - mx);
+        }
+      if (threadIdx.x < kRows) {
+        const int r = threadIdx.x;
+        float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = (threadIdx.x + i * kThreads) / Cfg::kJoinDims;
-      float mx = -INFINITY, sum = 0.0f;
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ctl->m[w][r]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ctl->m[w][r]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += ctl->m[w][r] == -INFINITY ? 0.0f : ctl->l[w][r] * ex2(ctl->m[w][r] - mx);
-      inv[i] = sum > 0.0f ? 1.0f / sum : 0.0f;
-      if (threadIdx.x % Cfg::kJoinDims == 0) {
+        for (int w = 0; w < kWarps; ++w) sum += ctl->m[w][r] == -INFINITY ? 0.0f : ctl->l[w][r] * ex2(ctl->m[w][r] - mx);
+        ctl->row_l[r] = sum > 0.0f ? 1.0f / sum : 0.0f;  // read after the next barrier
         if (!whole) {
           slot[kRows * D + 2 * r] = mx;
           slot[kRows * D + 2 * r + 1] = sum;
         } else if (p.lse && row0 + r < n_rows) {
           const int rr = row0 + r, tok = rr / group;
-          p.lse[static_cast<int64_t>(seq.first + tok) * a.n_heads + head * group + (rr - tok * group)] =
+          p.lse[static_cast<int64_t>(cur.seq.first + tok) * a.n_heads + cur.head * group + (rr - tok * group)] =
               sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
         }
       }
-    }
 #pragma unroll
-    for (int d0 = 0; d0 < D; d0 += Cfg::kJoinDims) {
+      for (int d0 = 0; d0 < D; d0 += Cfg::kJoinDims) {
 #pragma unroll
-      for (int mt = 0; mt < Cfg::kJoinDims / 16; ++mt)
+        for (int mt = 0; mt < Cfg::kJoinDims / 16; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int k = d0 / 16 + mt;
-            *reinterpret_cast<float2*>(join + (warp * kRows + nt * 8 + 2 * c + j) * Cfg::kJoinStride + 16 * mt + 2 * g) =
-                make_float2(o[k][nt][j] * wf[nt][j], o[k][nt][2 + j] * wf[nt][j]);
+            for (int j = 0; j < 2; ++j) {
+              const int k = d0 / 16 + mt;
+              *reinterpret_cast<float2*>(join + (warp * kRows + nt * 8 + 2 * c + j) * Cfg::kJoinStride + 16 * mt + 2 * g) =
+                  make_float2(o[k][nt][j] * wf[nt][j], o[k][nt][2 + j] * wf[nt][j]);
+            }
+        __syncthreads();
+        for (int e = threadIdx.x; e < kRows * Cfg::kJoinDims / 2; e += kThreads) {
+          const int r = e / (Cfg::kJoinDims / 2), d = 2 * (e % (Cfg::kJoinDims / 2));
+          float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 x = *reinterpret_cast<const float2*>(join + (w * kRows + r) * Cfg::kJoinStride + d);
+            sum.x += x.x;
+            sum.y += x.y;
           }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x + i * kThreads;
-        const int r = e / Cfg::kJoinDims, d = e % Cfg::kJoinDims;
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += join[(w * kRows + r) * Cfg::kJoinStride + d];
-        if (!whole) {
-          slot[r * D + d0 + d] = sum;
-        } else if (row0 + r < n_rows) {
-          const int rr = row0 + r, tok = rr / group;
-          p.out[(static_cast<int64_t>(seq.first + tok) * a.n_heads + head * group + (rr - tok * group)) * D + d0 + d] =
-              __bfloat16_as_ushort(__float2bfloat16_rn(sum * inv[i]));
+          if (!whole) {
+            *reinterpret_cast<float2*>(slot + r * D + d0 + d) = sum;
+          } else if (row0 + r < n_rows) {
+            const int rr = row0 + r, tok = rr / group;
+            const float inv = ctl->row_l[r];
+            *reinterpret_cast<uint32_t*>(
+                p.out + (static_cast<int64_t>(cur.seq.first + tok) * a.n_heads + cur.head * group + (rr - tok * group)) * D +
+                d0 + d) = pack_bf16x2(sum.x * inv, sum.y * inv);
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
+      if (!whole && t_first == 0 && threadIdx.x == 0)
+        p.desc[blockIdx.x] = make_int4(cur.s, cur.rt, cur.head, static_cast<int>((fu + cur.item_units - 1) / quota));
     }
-    if (!whole && t0 == 0 && threadIdx.x == 0)
-      p.desc[blockIdx.x] = make_int4(s, rt, head, static_cast<int>((first_unit + item_units - 1) / quota));
-
-    // ---- next item
-    at = first_unit + t1;
-    if (at >= u_end) break;
-    if (++head == a.n_kv) {
-      head = 0;
-      item0 = at;
-      if (++rt >= row_tiles(seq, kRows, group)) {
-        rt = 0;
-        do {
-          seq = load_seq(a, ++s);
-        } while (seq.n_new == 0 && s + 1 < a.S);
-      }
-      item_units = units_of(tile_keys(seq, rt, kRows, group));
+    if (!more) break;
+    // ---- the steps planned before become the present ones; plan the next
+    cur = nxt;
+    fc = fn;
+    more = advance(nxt, fc.units);
+    if (more) fn = plan(nxt);
+    else fn.use = fn.issue = 0u;
+    fresh = segment_ends;
+  }
+  // a wait that gave up leaves copies in flight: they land before the block may end
+  for (; inflight > 0; --inflight) {
+    mbar_wait_drain(&ctl->full[warp][stage], phase);
+    if (++stage == Cfg::kStages) {
+      stage = 0;
+      phase ^= 1u;
     }
   }
 }
@@ -636,11 +728,11 @@ cudaError_t launch(AttnParams p, const CUtensorMap& tmK, const CUtensorMap& tmV,
   if (e != cudaSuccess) return e;
   {
     LaunchScope scope(stream, "attn_kv8_kernel");
-    kern<<<blocks, kThreads, smem, stream>>>(tmK, tmV, p);
+    kern<<<blocks, Cfg::kThreads, smem, stream>>>(tmK, tmV, p);
   }
   e = cudaGetLastError();
   // no item has two units when a sequence cannot pass one: nothing to join
-  if (e != cudaSuccess || static_cast<int64_t>(p.a.max_pages) * p.a.page <= kUnit) return e;
+  if (e != cudaSuccess || static_cast<int64_t>(p.a.max_pages) * p.a.page <= Cfg::kUnit) return e;
   {
     LaunchScope scope(stream, "attn_kv8_join_kernel");
     attn_kv8_join_kernel<D, NT><<<blocks, 128, 0, stream>>>(p);
@@ -676,8 +768,8 @@ cudaError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, float sm_scale,
   const uint64_t rows = static_cast<uint64_t>(a.n_pages) * a.n_kv * a.page;
   const CUtensorMapSwizzle sw = a.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   CUtensorMap tmK, tmV;
-  cudaError_t e = make_tmap_2d(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, k_pages, rows, a.head_dim, a.head_dim, kTile, sw);
-  if (e == cudaSuccess) e = make_tmap_2d(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, v_pages, rows, a.head_dim, a.head_dim, kTile, sw);
+  cudaError_t e = make_tmap_2d(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, k_pages, rows, a.head_dim, a.head_dim, kBox, sw);
+  if (e == cudaSuccess) e = make_tmap_2d(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, v_pages, rows, a.head_dim, a.head_dim, kBox, sw);
   if (e != cudaSuccess) return e;
   const int nt = tiles_of(a);
   if (a.head_dim == 128)

@@ -13,8 +13,7 @@
 //  * A 32-code block of a row is 16 bytes: lane c of a row's four takes word c, so the two
 //    instructions of a block use 8 consecutive k a lane, activations are one 16-byte load,
 //    and the block's scale multiplies the fp32 sums of exactly that block.
-//  * Warps stream 16 rows x 256 k (2 KB boxes, 128-byte swizzle) through private rings of
-//    four; each takes an equal run of its block's (row tile, span) units and leaves a tile's
+//  * Warps stream 16 rows x 256 k (2 KB boxes, 128-byte swizzle) through private rings; each takes an equal run of its block's (row tile, span) units and leaves a tile's
 //    part in a slot of its own.  The CTAs of a cluster split k, so that a block's share of
 //    the activations stays in shared memory; their sums meet through distributed shared
 //    memory.  Parts are added in a fixed order.
@@ -23,20 +22,21 @@
 namespace ar {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;        // rows of a tile
 constexpr int kSpan = 256;       // k of a unit: 128 bytes of codes a row
 constexpr int kBoxBytes = kRows * 128;
-constexpr int kStages = 4;
-constexpr int kPassTiles = 16;   // row tiles between two reductions
+constexpr int kStagesMax = 4;    // boxes of a warp's ring, as many as the activations leave room for, at least 2
+constexpr int kPassTiles = 8;    // row tiles between two reductions
 constexpr int kSlots = kPassTiles + kWarps;  // (tile, warp) pairs along the warps' runs: tile + warp is unique
-constexpr int kRingBytes = kWarps * kStages * kBoxBytes;
-constexpr int kFixedBytes = kRingBytes + (kSlots + kPassTiles) * 128 * 4 + 1024 + 1024;
-constexpr int kActBytesMax = 226 * 1024 - kFixedBytes;
+constexpr int kRingBytes = kWarps * kBoxBytes;  // per stage
+constexpr int kFixedBytes = (kSlots + kPassTiles) * 128 * 4 + 1024 + 1024;  // slots, sums, barriers, alignment
+constexpr int kSmemMax = 226 * 1024;
+constexpr int kActBytesMax = kSmemMax - kFixedBytes - 2 * kRingBytes;
 
 struct DecCtl {
-  uint64_t full[kWarps][kStages];
+  uint64_t full[kWarps][kStagesMax];
   int abort_flag;
 };
 
@@ -48,6 +48,7 @@ struct DecParams {
   int spans;       // of 256 k, in all
   int spans_cta;   // of a CTA (the last may have fewer)
   int tiles;       // row tiles
+  int stages;
   int wide;        // a row's scale bytes of a span are one aligned 8-byte word
 };
 
@@ -94,10 +95,10 @@ template <int CL>
 __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_constant__ CUtensorMap tmW, const DecParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* slots = reinterpret_cast<float*>(smem + kRingBytes);       // [kSlots][16 rows][8 tokens]
+  float* slots = reinterpret_cast<float*>(smem + p.stages * kRingBytes);  // [kSlots][16 rows][8 tokens]
   float* sums = slots + kSlots * 128;                               // [kPassTiles][16][8]
   DecCtl* ctl = reinterpret_cast<DecCtl*>(sums + kPassTiles * 128);
-  float* factor = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ctl) + 512);  // [spans_cta][8 tokens]
+  float* factor = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ctl) + 1024);  // [spans_cta][8 tokens]
   uint8_t* act = reinterpret_cast<uint8_t*>(factor + p.spans_cta * 8);              // [span][block][T][64 bytes]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -107,12 +108,13 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
   const int C = s1 - s0;
   const int tile0 = static_cast<int>(static_cast<int64_t>(p.tiles) * cluster / clusters);
   const int tile1 = static_cast<int>(static_cast<int64_t>(p.tiles) * (cluster + 1) / clusters);
-  uint8_t* ring = smem + warp * kStages * kBoxBytes;
+  const int stages = p.stages;
+  uint8_t* ring = smem + warp * stages * kBoxBytes;
   const int blocks_row = p.K / 32;
 
   if (threadIdx.x == 0) {
     for (int w = 0; w < kWarps; ++w)
-      for (int s = 0; s < kStages; ++s) mbar_init(&ctl->full[w][s], 1);
+      for (int s = 0; s < kStagesMax; ++s) mbar_init(&ctl->full[w][s], 1);
     ctl->abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmW);
@@ -125,23 +127,28 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
     const int nt = min(kPassTiles, tile1 - pass);
     const int U = nt * C;
     const int u0 = U * warp / kWarps, u1 = U * (warp + 1) / kWarps;
-    // unit u: tile pass + u / C, span s0 + u % C
-    auto issue = [&](int u, uint32_t st) {
-      const int tl = u / C, sp = s0 + (u - tl * C);
-      const int row = (pass + tl) * kRows;
+    // unit u: tile pass + u / C, span s0 + u % C; the copies' own place runs ahead of the sums'
+    int next = u0, i_tile = C > 0 ? u0 / C : 0, i_span = C > 0 ? u0 % C : 0;
+    auto issue = [&](uint32_t st) {
+      const int row = (pass + i_tile) * kRows, sp = s0 + i_span;
       if (lane == 0) {
         mbar_arrive_expect_tx(&ctl->full[warp][st], kBoxBytes);
         tma_load_2d(ring + st * kBoxBytes, &tmW, &ctl->full[warp][st], sp * 32, row);
       }
-      if (lane < kRows && row + lane < p.N)  // the scales are read later: bring them into L2 with the codes
+      // the scales are read later: bring them into L2 with the codes (32 bytes are four spans)
+      if ((next == u0 || (sp & 3) == 0) && lane < kRows && row + lane < p.N)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.scales + static_cast<int64_t>(row + lane) * blocks_row + sp * 8));
+      ++next;
+      if (++i_span == C) {
+        i_span = 0;
+        ++i_tile;
+      }
     };
-    int next = u0;
     uint32_t ahead = stage;
     if (alive) {
-      for (int i = 0; i < kStages && next < u1; ++i, ++next) {
-        issue(next, ahead);
-        ahead = ahead + 1 == kStages ? 0 : ahead + 1;
+      for (int i = 0; i < stages && next < u1; ++i) {
+        issue(ahead);
+        ahead = ahead + 1 == stages ? 0 : ahead + 1;
       }
     }
     if (pass == tile0) {
@@ -186,38 +193,50 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
     float tot[4] = {0.f, 0.f, 0.f, 0.f};
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     const uint32_t act_lane = smem_u32(act) + min(g, p.T - 1) * 64 + c * 16;
+    const uint32_t act_block = p.T * 64;
     const uint32_t lane_off = g * 128 + c * 4, flip = g << 4;
-    auto load_scales = [&](int u, uint2 (&sc)[2]) {
-      const int tl = u / C, sp = s0 + (u - tl * C);
+    int tl = C > 0 ? u0 / C : 0, sp = C > 0 ? u0 % C : 0;
+    const uint8_t* rows[2];  // this lane's two rows of scales, at the CTA's first span
+    auto set_rows = [&](int tile) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        rows[h] = p.scales + static_cast<int64_t>(min((pass + tile) * kRows + g + 8 * h, p.N - 1)) * blocks_row + s0 * 8;
+    };
+    auto load_scales = [&](int span, uint2 (&sc)[2]) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = min((pass + tl) * kRows + g + 8 * h, p.N - 1);
-        const uint8_t* src = p.scales + static_cast<int64_t>(row) * blocks_row + sp * 8;
+        const uint8_t* src = rows[h] + span * 8;
         if (p.wide) {
           sc[h] = __ldg(reinterpret_cast<const uint2*>(src));
         } else {
           uint32_t v[2] = {0u, 0u};
 #pragma unroll
           for (int b = 0; b < 8; ++b)
-            if (sp * 8 + b < blocks_row) v[b >> 2] |= static_cast<uint32_t>(__ldg(src + b)) << (8 * (b & 3));
+            if ((s0 + span) * 8 + b < blocks_row) v[b >> 2] |= static_cast<uint32_t>(__ldg(src + b)) << (8 * (b & 3));
           sc[h] = make_uint2(v[0], v[1]);
         }
       }
     };
     uint2 sc[2], sn[2];
-    if (u0 < u1) load_scales(u0, sc);
+    if (u0 < u1) {
+      set_rows(tl);
+      load_scales(sp, sc);
+    }
     for (int u = u0; alive && u < u1; ++u) {
-      const int tl = u / C, sp = u - tl * C;
+      const bool last = sp == C - 1;
       sn[0] = sc[0];
       sn[1] = sc[1];
-      if (u + 1 < u1) load_scales(u + 1, sn);
+      if (u + 1 < u1) {  // the next unit's scales, while this one is summed
+        if (last) set_rows(tl + 1);
+        load_scales(last ? 0 : sp + 1, sn);
+      }
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[warp][stage], phase, &ctl->abort_flag))) {
         alive = false;
         // copies in flight land before the block may end
         uint32_t st = stage, ph = phase;
         for (int i = u; i < next; ++i) {
           mbar_wait_drain(&ctl->full[warp][st], ph);
-          if (++st == kStages) {
+          if (++st == stages) {
             st = 0;
             ph ^= 1u;
           }
@@ -225,14 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
         break;
       }
       const uint32_t w = smem_u32(ring + stage * kBoxBytes) + lane_off;
-      const uint32_t ab = act_lane + sp * 8 * p.T * 64;
+      uint32_t ab = act_lane + sp * 8 * act_block;
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t bf[2] = {0u, 0u};
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         const uint32_t off = static_cast<uint32_t>(b << 4) ^ flip;
         const uint32_t x0 = lds32(w + off), x1 = lds32(w + off + 1024);
-        const uint4 a = lds128(ab + b * p.T * 64);
+        const uint4 a = lds128(ab);
+        ab += act_block;
         float d[4];
         uint32_t h0[4], h1[4];
         e2m1x8_f16(x0, h0);
@@ -255,21 +275,22 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
       tot[2] = fmaf(acc[2], fa.x, tot[2]);
       tot[3] = fmaf(acc[3], fa.y, tot[3]);
       __syncwarp();  // the slot has been read
-      if (next < u1) {
-        issue(next, stage);
-        ++next;
-      }
-      if (++stage == kStages) {
+      if (next < u1) issue(stage);
+      if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
       }
       sc[0] = sn[0];
       sc[1] = sn[1];
-      if (sp == C - 1 || u + 1 == u1) {  // this warp's part of the tile ends
+      if (last || u + 1 == u1) {  // this warp's part of the tile ends
         float* slot = slots + (tl + warp) * 128;
         *reinterpret_cast<float2*>(slot + g * 8 + 2 * c) = make_float2(tot[0], tot[1]);
         *reinterpret_cast<float2*>(slot + (g + 8) * 8 + 2 * c) = make_float2(tot[2], tot[3]);
         tot[0] = tot[1] = tot[2] = tot[3] = 0.f;
+      }
+      if (++sp == C) {
+        sp = 0;
+        ++tl;
       }
     }
     __syncthreads();
@@ -331,7 +352,7 @@ cudaError_t launch(const CUtensorMap& tmW, const DecParams& p, int smem, cudaStr
   int clusters = dev < 64 ? resident[dev].load(std::memory_order_relaxed) : 0;
   if (clusters == 0) {
     cfg.gridDim = dim3(num_sms() / CL * CL);
-    cfg.dynamicSmemBytes = 226 * 1024;
+    cfg.dynamicSmemBytes = kSmemMax;
     e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
     if (e != cudaSuccess) return e;
     if (clusters < 1) return cudaErrorInvalidConfiguration;
@@ -367,7 +388,9 @@ cudaError_t launch_mxfp4_dec(const uint16_t* A, int T, const uint8_t* codes, con
   if (p.spans >= 4 && (act(2) > kActBytesMax || 2 * p.tiles < num_sms())) cl = 4;
   if (act(cl) > kActBytesMax) return cudaErrorNotSupported;
   p.spans_cta = (p.spans + cl - 1) / cl;
-  const int smem = kFixedBytes + act(cl);
+  p.stages = (kSmemMax - kFixedBytes - act(cl)) / kRingBytes;
+  if (p.stages > kStagesMax) p.stages = kStagesMax;
+  const int smem = kFixedBytes + p.stages * kRingBytes + act(cl);
   CUtensorMap tmW;
   cudaError_t e = make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, codes, static_cast<uint64_t>(N),
                                static_cast<uint64_t>(K) / 8, 32, kRows, CU_TENSOR_MAP_SWIZZLE_128B);

@@ -152,6 +152,19 @@ def test_attention_split_over_blocks(ar, n_heads, n_kv, d, lens):
     _check(c, q, cu, got)
 
 
+@pytest.mark.parametrize("n_heads,n_kv,d", [(8, 8, 128), (64, 4, 64), (24, 1, 128)])
+def test_attention_many_short_sequences(ar, n_heads, n_kv, d):
+    """Many items to a block, most of them too short to give every warp a step, some in two pieces."""
+    rng = np.random.default_rng(n_heads)
+    lens = [int(x) for x in rng.choice([1, 3, 20, 40, 200, 300, 700], 700, p=[.3, .2, .2, .1, .1, .05, .05])]
+    c = Cache(lens, n_heads, n_kv, d, 16, 3)
+    cu, cud, ld = _index([1] * len(lens), lens)
+    q = torch.from_numpy(c.rng.normal(size=(len(lens), n_heads * d)).astype(np.float32)).bfloat16().cuda()
+    out = _attend(ar, c, q, cud, ld, 1)
+    assert ar.ar_get_device_status() == ar.AR_OK
+    _check(c, q, cu, out)
+
+
 def test_attention_scales_that_differ_widely(ar):
     """Value scales 2^20 apart between pages, key scales that make some scores large: the weights' f16 rounding stays
     relative to the largest contribution."""
