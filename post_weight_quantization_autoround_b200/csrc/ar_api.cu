@@ -1295,10 +1295,9 @@ ar_status ar_kv8_append(const ar_kv8_cfg* cfg, const uint16_t* qkv, int64_t T, c
   return end_call();
 }
 
-// units of 128 keys that a call can have at most must fit 31 bits
-static ar_status check_kv8_units(const Kv8Args& a) {
-  const double tiles = static_cast<double>(a.T) * (a.n_heads / a.n_kv) / 8.0 + a.S;
-  if (tiles * a.n_kv * (static_cast<double>(a.max_pages) * a.page / 128.0 + 1.0) >= 2147483648.0)
+// the steps that a call can have at most must fit 31 bits
+static ar_status check_kv8_steps(const Kv8Args& a) {
+  if (attn_kv8_steps(a) >= 2147483648.0)
     return fail(AR_ERR_UNSUPPORTED, "too many row tiles times keys for one call: split the batch");
   return AR_OK;
 }
@@ -1321,7 +1320,7 @@ ar_status ar_attention_kv8(const ar_kv8_cfg* cfg, const uint16_t* q, int64_t T, 
   if (st != AR_OK) return st;
   st = check_kv8_pointers(a, q, out, k_pages, v_pages, k_scales, v_scales);
   if (st != AR_OK) return st;
-  st = check_kv8_units(a);
+  st = check_kv8_steps(a);
   if (st != AR_OK) return st;
   if (lse && !aligned4(lse)) return fail(AR_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   if (!(sm_scale >= 0.0f) || !(sm_scale < 1e30f)) return fail(AR_ERR_INVALID_ARG, "sm_scale must be finite and >= 0 (0: 1/sqrt(head_dim))");

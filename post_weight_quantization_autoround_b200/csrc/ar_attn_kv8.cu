@@ -20,16 +20,16 @@
 //  * S^T leaves the tensor core with tokens along lanes' rows; movmatrix transposes the
 //    8 x 8 blocks into the B operand of O^T.  V^T comes from ldmatrix.trans on byte pairs:
 //    one byte permute separates even and odd dimensions.
-//  * Each of a block's warps streams its own tiles of 32 tokens (4 KB of keys and of values
-//    at d = 128; TMA boxes with the hardware swizzle, so neither read conflicts)
-//    through a private ring; nothing but the end of an item synchronises the block, and the
-//    copies run on into the next item meanwhile (its pages and scales are looked up an
-//    item ahead).  Two blocks of 6 warps share an SM up to 8 rows.
-//  * The work is the list of (sequence, row tile, head, 192 or 256 tokens) units.  Every block takes
-//    an equal run of it, found from the lengths on the device (the host does not know them,
-//    and a captured graph keeps working as they grow).  A row tile split between blocks is
-//    joined by a second kernel from unnormalised sums in the workspace, in block order: no
-//    atomics, the same result every time.
+//  * The work is the list of (sequence, row tile, head, 32 tokens) steps.  Every warp takes an
+//    equal run of it, found from the lengths on the device (the host does not know them,
+//    and a captured graph keeps working as they grow), and streams it (4 KB of keys and of
+//    values a step at d = 128; TMA boxes with the hardware swizzle, so neither read
+//    conflicts) through a private ring: no barrier between warps.  Pages and scales are
+//    looked up an item ahead and the copies run on past an item's end.
+//  * An item within one warp's run goes straight to the output.  One that warps share is
+//    joined from unnormalised sums in the workspace, by its block at the end of the
+//    block's run, and by a second kernel where several blocks share it; always in the
+//    order of the tokens: no atomics, the same result every time.
 #include "ar_internal.h"
 
 namespace ar {
@@ -47,22 +47,23 @@ struct AttnCfg {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kHalves = NT == 4 ? 1 : 2;     // boxes of 16 tokens in a warp's step
   static constexpr int kTile = kBox * kHalves;        // tokens of a step
-  static constexpr int kUnit = kWarps * kTile;        // tokens of a work unit
-  static constexpr int kStages = D == 128 ? (NT == 4 ? 4 : 2) : 4;
+  static constexpr int kStages = D == 128 ? (NT == 4 ? 6 : NT == 2 ? 3 : 2) : 4;
   static constexpr int kBoxBytes = kBox * D;
   static constexpr int kTileBytes = kTile * D;        // of keys, and of values
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kJoinDims = 32;                // dimensions joined per round
-  static constexpr int kJoinStride = kJoinDims + 4;   // floats
-  static constexpr int kJoinBytes = kWarps * kRows * kJoinStride * 4;
   static constexpr int kSlotFloats = kRows * (D + 2); // a partial result: sums, then maximum and row sum per row
 };
 
+// a part of an item that one warp computed
+struct Part {
+  uint32_t item0;  // first step of the item
+  int s, rt, head, steps;  // the item; steps = 0: no part
+};
+
 struct AttnCtl {
-  uint64_t full[kMaxWarps][4];
-  float m[kMaxWarps][32], l[kMaxWarps][32];  // per warp and row
-  float row_l[32];                           // of the block: 1 / row sum
+  uint64_t full[kMaxWarps][6];
+  Part part[kMaxWarps][2];  // of an item begun before the warp's run; of one that goes on after it
   int abort_flag;
 };
 
@@ -73,7 +74,8 @@ struct AttnParams {
   const uint8_t* vs;
   uint16_t* out;
   float* lse;
-  float* slots;  // [blocks][2][kSlotFloats]
+  float* slots;       // [blocks][2][kSlotFloats], like a warp's parts
+  float* warp_slots;  // [blocks][warps][2][kSlotFloats]
   int4* desc;    // [blocks]: {sequence, row tile, head, last block} of the item whose first part is the block's, or x = -1
   float scale_log2;
 };
@@ -101,9 +103,9 @@ __device__ __forceinline__ int tile_keys(const Seq& q, int rt, int rows, int gro
   return max(0, q.len - q.n_new + last + 1);
 }
 
-template <int UNIT>
-__device__ __forceinline__ int units_of(int keys) {
-  return keys <= UNIT ? 1 : (keys + UNIT - 1) / UNIT;
+template <int TILE>
+__device__ __forceinline__ int steps_of(int keys) {
+  return keys <= TILE ? 1 : (keys + TILE - 1) / TILE;
 }
 
 __device__ __forceinline__ int row_tiles(const Seq& q, int rows, int group) {
@@ -163,21 +165,33 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {
   return static_cast<uint32_t>(row * D + ((D == 128 ? (chunk ^ (row & 7)) : (chunk ^ ((row >> 1) & 3))) << 4));
 }
 
-// where a block's run of units stands
+// 4 dimensions of a row, and its log-sum-exp with the first of them
+template <int D>
+__device__ __forceinline__ void write_row(const AttnParams& p, const Seq& seq, int head, int group, int rr, int d, float4 acc,
+                                          float mx, float sum) {
+  const int tok = rr / group;
+  const int64_t row = static_cast<int64_t>(seq.first + tok) * p.a.n_heads + head * group + (rr - tok * group);
+  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+  *reinterpret_cast<uint2*>(p.out + row * D + d) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (p.lse && d == 0) p.lse[row] = sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+// where a warp's run of steps stands
 struct Pos {
   int s, rt, head;   // sequence, row tile, key/value head
   Seq seq;
-  int item_units;    // units of the row tile (for each head)
-  uint32_t item0;    // first unit of the row tile's first head
-  uint32_t at;       // next unit
+  int item_steps;    // steps of the row tile (for each head)
+  uint32_t item0;    // first step of the row tile's first head
+  uint32_t at;       // next step
 };
 
-// the steps of one warp in up to kChunk units of an item, one a lane
+// up to kChunk steps of a warp in one item, one a lane
 struct Steps {
   int row[2];      // first row of the step's boxes in the cache, -1: nothing to read
   uint32_t exps;   // scale codes: key, value of the first box, key, value of the second
   uint32_t use, issue;  // steps still to be computed, still to be copied
-  int units;
+  int n;
 };
 
 template <int D, int NT>
@@ -185,15 +199,14 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
     attn_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using Cfg = AttnCfg<D, NT>;
   constexpr int kRows = Cfg::kRows, kWarps = Cfg::kWarps, kThreads = Cfg::kThreads, kHalves = Cfg::kHalves;
-  constexpr int kTile = Cfg::kTile, kUnit = Cfg::kUnit;
+  constexpr int kTile = Cfg::kTile;
   constexpr int kKs = D / 16;      // k-steps of S^T
   constexpr int kMt = D / 16;      // 16-dimension tiles of O^T
   constexpr int kQr = D / 64;      // 16-byte loads of a K row per lane
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* join = reinterpret_cast<float*>(smem + Cfg::kRingBytes);
-  AttnCtl* ctl = reinterpret_cast<AttnCtl*>(smem + Cfg::kRingBytes + Cfg::kJoinBytes);
-  uint32_t* prefix = reinterpret_cast<uint32_t*>(ctl + 1);  // [S + 1] units before each sequence
+  AttnCtl* ctl = reinterpret_cast<AttnCtl*>(smem + Cfg::kRingBytes);
+  uint32_t* prefix = reinterpret_cast<uint32_t*>(ctl + 1);  // [S + 1] steps before each sequence
   const Kv8Args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -208,12 +221,12 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  // units of every sequence: a thread each where it is one row tile, else a warp each
+  // steps of every sequence: a thread each where it is one row tile, else a warp each
   if (a.max_new * group <= kRows) {
     for (int s = threadIdx.x; s < a.S; s += kThreads) {
       const Seq q = load_seq(a, s);
       uint32_t u = 0;
-      for (int rt = 0; rt < row_tiles(q, kRows, group); ++rt) u += units_of<kUnit>(tile_keys(q, rt, kRows, group));
+      for (int rt = 0; rt < row_tiles(q, kRows, group); ++rt) u += steps_of<kTile>(tile_keys(q, rt, kRows, group));
       prefix[s + 1] = u * a.n_kv;
     }
   } else {
@@ -221,7 +234,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
       const Seq q = load_seq(a, s);
       const int nrt = row_tiles(q, kRows, group);
       uint32_t u = 0;
-      for (int rt = lane; rt < nrt; rt += 32) u += units_of<kUnit>(tile_keys(q, rt, kRows, group));
+      for (int rt = lane; rt < nrt; rt += 32) u += steps_of<kTile>(tile_keys(q, rt, kRows, group));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
       if (lane == 0) prefix[s + 1] = u * a.n_kv;
@@ -244,14 +257,16 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
   }
   __syncthreads();
   const uint32_t total = prefix[a.S];
-  const uint32_t quota = (total + gridDim.x - 1) / gridDim.x;
-  const uint32_t u_begin = min(total, blockIdx.x * quota), u_end = min(total, u_begin + quota);
+  const uint32_t quota = (total + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);  // steps of a warp
+  const uint32_t b_begin = min(total, blockIdx.x * kWarps * quota), b_end = min(total, b_begin + kWarps * quota);
+  const uint32_t u_begin = min(total, b_begin + warp * quota), u_end = min(total, u_begin + quota);
   if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if (u_begin >= u_end) return;
+  if (lane < 2) ctl->part[warp][lane].steps = 0;
+  if (b_begin >= b_end) return;
 
   // where the run starts
-  Pos cur;
-  {
+  Pos cur{};
+  if (u_begin < u_end) {
     int lo = 0, hi = a.S - 1;
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
@@ -263,18 +278,18 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
     cur.at = u_begin;
     cur.item0 = prefix[lo];
     for (cur.rt = 0;; ++cur.rt) {
-      cur.item_units = units_of<kUnit>(tile_keys(cur.seq, cur.rt, kRows, group));
-      const uint32_t next = cur.item0 + static_cast<uint32_t>(cur.item_units) * a.n_kv;
+      cur.item_steps = steps_of<kTile>(tile_keys(cur.seq, cur.rt, kRows, group));
+      const uint32_t next = cur.item0 + static_cast<uint32_t>(cur.item_steps) * a.n_kv;
       if (next > cur.at) break;
       cur.item0 = next;
     }
-    cur.head = static_cast<int>((cur.at - cur.item0) / cur.item_units);
+    cur.head = static_cast<int>((cur.at - cur.item0) / cur.item_steps);
   }
-  auto first_unit = [&](const Pos& q) { return q.item0 + static_cast<uint32_t>(q.head) * q.item_units; };
-  auto advance = [&](Pos& q, int units) {  // false at the end of the block's run
-    q.at += units;
+  auto first_step = [&](const Pos& q) { return q.item0 + static_cast<uint32_t>(q.head) * q.item_steps; };
+  auto advance = [&](Pos& q, int n) {  // false at the end of the warp's run
+    q.at += n;
     if (q.at >= u_end) return false;
-    if (q.at == first_unit(q) + q.item_units) {
+    if (q.at == first_step(q) + q.item_steps) {
       if (++q.head == a.n_kv) {
         q.head = 0;
         q.item0 = q.at;
@@ -284,24 +299,24 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
             q.seq = load_seq(a, ++q.s);
           } while (q.seq.n_new == 0 && q.s + 1 < a.S);
         }
-        q.item_units = units_of<kUnit>(tile_keys(q.seq, q.rt, kRows, group));
+        q.item_steps = steps_of<kTile>(tile_keys(q.seq, q.rt, kRows, group));
       }
     }
     return true;
   };
-  // the next steps at q: lane i looks up pages and scales of unit i
+  // the next steps at q: lane i looks up pages and scales of step i
   auto plan = [&](const Pos& q) {
     Steps f;
-    const uint32_t fu = first_unit(q);
-    const int unit0 = static_cast<int>(q.at - fu);
-    f.units = static_cast<int>(min(min(u_end, fu + q.item_units) - q.at, static_cast<uint32_t>(kChunk)));
+    const uint32_t fu = first_step(q);
+    const int step0 = static_cast<int>(q.at - fu);
+    f.n = static_cast<int>(min(min(u_end, fu + q.item_steps) - q.at, static_cast<uint32_t>(kChunk)));
     const int keys = tile_keys(q.seq, q.rt, kRows, group);
     f.exps = 0u;
     f.row[0] = f.row[1] = -1;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      const int t = (unit0 + lane) * kUnit + warp * kTile + h * kBox;
-      if (lane < f.units && t < keys) {
+      const int t = (step0 + lane) * kTile + h * kBox;
+      if (lane < f.n && t < keys) {
         const int pg = __ldg(a.table + static_cast<int64_t>(q.s) * a.max_pages + t / a.page);
         if (pg >= 0 && pg < a.n_pages) {
           const int64_t ph = static_cast<int64_t>(pg) * a.n_kv + q.head;
@@ -339,12 +354,15 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
     ++inflight;
   };
 
-  Steps fc = plan(cur);
+  Steps fc{}, fn{};
   Pos nxt = cur;
-  bool more = advance(nxt, fc.units);
-  Steps fn;
-  if (more) fn = plan(nxt);
-  else fn.use = fn.issue = 0u;
+  bool more = false;
+  if (u_begin < u_end) {
+    fc = plan(cur);
+    nxt = cur;
+    more = advance(nxt, fc.n);
+    if (more) fn = plan(nxt);
+  }
   // Copies run ahead into the next steps planned, past the end of an item.  Called wherever a slot or new steps
   // come free: after a step, and after planning (a warp may have had nothing to do in two plans running).
   auto refill = [&]() {
@@ -359,17 +377,17 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
   int lim[NT][2];
   float o[kMt][NT][4];
   float m[NT][2], l[NT][2];
-  int t_first = 0, full_below = 0, keys = 0;  // of the segment: its first unit in the item, tokens every row sees, keys
+  int t_first = 0, full_below = 0, keys = 0;  // of the part: its first step in the item, tokens every row sees, keys
   bool fresh = true;
 
-  for (;;) {
+  while (u_begin < u_end) {
     refill();
     const int row0 = cur.rt * kRows;
     const int n_rows = cur.seq.n_new * group;
     if (fresh) {
       // ---- a new item: queries as B operand registers, normalised; a row's factor to log2 units
       const int start = cur.seq.len - cur.seq.n_new;
-      t_first = static_cast<int>(cur.at - first_unit(cur));
+      t_first = static_cast<int>(cur.at - first_step(cur));
       keys = tile_keys(cur.seq, cur.rt, kRows, group);
       full_below = start + row0 / group + 1;
 #pragma unroll
@@ -422,12 +440,12 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
           for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.f;
     }
 
-    const int unit0 = static_cast<int>(cur.at - first_unit(cur));
+    const int step0 = static_cast<int>(cur.at - first_step(cur));
     while (alive && fc.use) {
       const int i = __ffs(fc.use) - 1;
       fc.use &= fc.use - 1;
       const uint32_t exps = __shfl_sync(0xFFFFFFFFu, fc.exps, i);
-      const int tb = (unit0 + i) * kUnit + warp * kTile;  // first token of the step
+      const int tb = (step0 + i) * kTile;  // first token of the step
       // a step whose boxes are not both there: past the keys, or a page that is not in the pool
       const uint32_t have = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, (fc.row[0] >= 0 ? 1 : 0) | (fc.row[1] >= 0 ? 2 : 0), i));
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[warp][stage], phase, &ctl->abort_flag))) {
@@ -563,97 +581,58 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
       refill();
     }
 
-    const uint32_t fu = first_unit(cur);
-    const int t_end = static_cast<int>(cur.at - fu) + fc.units;  // units of the item done so far
-    const bool segment_ends = fu + t_end == u_end || t_end == cur.item_units;
-    if (segment_ends) {
-      // ---- join the warps: maximum and sum of every row, then the sums of 32 dimensions a round
+    const uint32_t fu = first_step(cur);
+    const int t_end = static_cast<int>(cur.at - fu) + fc.n;  // steps of the item done so far
+    const bool part_ends = fu + t_end == u_end || t_end == cur.item_steps;
+    if (part_ends) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], x);
-          if (g == 0) {
-            ctl->m[warp][nt * 8 + 2 * c + j] = m[nt][j];
-            ctl->l[warp][nt * 8 + 2 * c + j] = l[nt][j];
+      if (t_first == 0 && t_end == cur.item_steps) {
+        // the whole item: straight to the output
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int rr = row0 + nt * 8 + 2 * c + j;
+            if (rr >= n_rows) continue;
+            const int tok = rr / group;
+            const int64_t row = static_cast<int64_t>(cur.seq.first + tok) * a.n_heads + cur.head * group + (rr - tok * group);
+            const float inv = l[nt][j] > 0.0f || l[nt][j] != l[nt][j] ? 1.0f / l[nt][j] : 0.0f;
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt)
+              *reinterpret_cast<uint32_t*>(p.out + row * D + 16 * mt + 2 * g) =
+                  pack_bf16x2(o[mt][nt][j] * inv, o[mt][nt][2 + j] * inv);
+            if (p.lse && g == 0)
+              p.lse[row] = l[nt][j] > 0.0f ? (m[nt][j] + log2f(l[nt][j])) * 0.6931471805599453f : -INFINITY;
           }
-        }
-      __syncthreads();
-      const bool whole = t_first == 0 && t_end == cur.item_units;
-      float* slot = p.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (t_first == 0 ? 1 : 0)) * Cfg::kSlotFloats;
-      float wf[NT][2];  // this warp's factor to the block's maximum
+      } else {
+        const int k = t_first == 0 ? 1 : 0;
+        float* slot = p.warp_slots + ((static_cast<int64_t>(blockIdx.x) * kWarps + warp) * 2 + k) * Cfg::kSlotFloats;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float mx = -INFINITY;
+          for (int j = 0; j < 2; ++j) {
+            const int r = nt * 8 + 2 * c + j;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ctl->m[w][nt * 8 + 2 * c + j]);
-          wf[nt][j] = m[nt][j] == -INFINITY ? 0.0f : ex2(m[nt][j] - mx);
-        }
-      if (threadIdx.x < kRows) {
-        const int r = threadIdx.x;
-        float mx = -INFINITY, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ctl->m[w][r]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += ctl->m[w][r] == -INFINITY ? 0.0f : ctl->l[w][r] * ex2(ctl->m[w][r] - mx);
-        ctl->row_l[r] = sum > 0.0f ? 1.0f / sum : 0.0f;  // read after the next barrier
-        if (!whole) {
-          slot[kRows * D + 2 * r] = mx;
-          slot[kRows * D + 2 * r + 1] = sum;
-        } else if (p.lse && row0 + r < n_rows) {
-          const int rr = row0 + r, tok = rr / group;
-          p.lse[static_cast<int64_t>(cur.seq.first + tok) * a.n_heads + cur.head * group + (rr - tok * group)] =
-              sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-        }
+            for (int mt = 0; mt < kMt; ++mt)
+              *reinterpret_cast<float2*>(slot + r * D + 16 * mt + 2 * g) = make_float2(o[mt][nt][j], o[mt][nt][2 + j]);
+            if (g == 0) *reinterpret_cast<float2*>(slot + kRows * D + 2 * r) = make_float2(m[nt][j], l[nt][j]);
+          }
+        if (lane == 0) ctl->part[warp][k] = Part{fu, cur.s, cur.rt, cur.head, cur.item_steps};
       }
-#pragma unroll
-      for (int d0 = 0; d0 < D; d0 += Cfg::kJoinDims) {
-#pragma unroll
-        for (int mt = 0; mt < Cfg::kJoinDims / 16; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int k = d0 / 16 + mt;
-              *reinterpret_cast<float2*>(join + (warp * kRows + nt * 8 + 2 * c + j) * Cfg::kJoinStride + 16 * mt + 2 * g) =
-                  make_float2(o[k][nt][j] * wf[nt][j], o[k][nt][2 + j] * wf[nt][j]);
-            }
-        __syncthreads();
-        for (int e = threadIdx.x; e < kRows * Cfg::kJoinDims / 2; e += kThreads) {
-          const int r = e / (Cfg::kJoinDims / 2), d = 2 * (e % (Cfg::kJoinDims / 2));
-          float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 x = *reinterpret_cast<const float2*>(join + (w * kRows + r) * Cfg::kJoinStride + d);
-            sum.x += x.x;
-            sum.y += x.y;
-          }
-          if (!whole) {
-            *reinterpret_cast<float2*>(slot + r * D + d0 + d) = sum;
-          } else if (row0 + r < n_rows) {
-            const int rr = row0 + r, tok = rr / group;
-            const float inv = ctl->row_l[r];
-            *reinterpret_cast<uint32_t*>(
-                p.out + (static_cast<int64_t>(cur.seq.first + tok) * a.n_heads + cur.head * group + (rr - tok * group)) * D +
-                d0 + d) = pack_bf16x2(sum.x * inv, sum.y * inv);
-          }
-        }
-        __syncthreads();
-      }
-      if (!whole && t_first == 0 && threadIdx.x == 0)
-        p.desc[blockIdx.x] = make_int4(cur.s, cur.rt, cur.head, static_cast<int>((fu + cur.item_units - 1) / quota));
     }
     if (!more) break;
     // ---- the steps planned before become the present ones; plan the next
     cur = nxt;
     fc = fn;
-    more = advance(nxt, fc.units);
+    more = advance(nxt, fc.n);
     if (more) fn = plan(nxt);
     else fn.use = fn.issue = 0u;
-    fresh = segment_ends;
+    fresh = part_ends;
   }
   // a wait that gave up leaves copies in flight: they land before the block may end
   for (; inflight > 0; --inflight) {
@@ -663,14 +642,79 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
       phase ^= 1u;
     }
   }
+
+  // ---- items that several warps of the block share: a warp joins each from the parts in the workspace
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the second kernel may be set up (it waits for this one's end)
+  __syncthreads();
+  constexpr int kVec = D / 4;                     // 16-byte pieces of a row
+  constexpr int kPieces = kRows * kVec / 32;      // a warp's worth of an item
+  int at = 0;
+  for (int piece0 = 0; at < 2 * kWarps; piece0 += kPieces) {
+    while (at < 2 * kWarps && ctl->part[at >> 1][at & 1].steps == 0) ++at;
+    if (at >= 2 * kWarps) break;
+    // the item's parts: this warp's slot, then the first slots of the warps after it
+    const Part it = ctl->part[at >> 1][at & 1];
+    const int from = at;
+    int last = at;
+    for (++at; at < 2 * kWarps; ++at) {
+      if (ctl->part[at >> 1][at & 1].steps == 0) continue;
+      if (ctl->part[at >> 1][at & 1].item0 != it.item0) break;
+      last = at;
+    }
+    const bool whole = it.item0 >= b_begin && it.item0 + it.steps <= b_end;
+    const Seq seq = load_seq(a, it.s);
+    const int row0 = it.rt * kRows, n_rows = min(kRows, seq.n_new * group - row0);
+    float* slot = p.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (it.item0 >= b_begin ? 1 : 0)) * Cfg::kSlotFloats;
+    const float* base = p.warp_slots + (static_cast<int64_t>(blockIdx.x) * kWarps * 2 + from) * Cfg::kSlotFloats;
+    // part j: `from` itself, then every second slot (a warp has two)
+    const int parts = 1 + (last >> 1) - (from >> 1);
+    auto part_at = [&](int j) { return base + (j == 0 ? 0 : 2 * j - (from & 1)) * Cfg::kSlotFloats; };
+    for (int piece = (warp + kWarps - piece0 % kWarps) % kWarps; piece < kPieces; piece += kWarps) {
+      const int e = piece * 32 + lane, r = e / kVec, d = 4 * (e % kVec);
+      // all loads first: a join waits for one of them, not for each
+      float2 ml[kWarps];
+      float4 x[kWarps];
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.0f);
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < parts) {
+          ml[j] = *reinterpret_cast<const float2*>(part_at(j) + kRows * D + 2 * r);
+          x[j] = *reinterpret_cast<const float4*>(part_at(j) + r * D + d);
+        }
+      }
+      float mx = -INFINITY, sum = 0.0f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) mx = fmaxf(mx, ml[j].x);
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        const float f = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - mx);
+        sum = fmaf(ml[j].y, f, sum);
+        acc.x = fmaf(x[j].x, f, acc.x);
+        acc.y = fmaf(x[j].y, f, acc.y);
+        acc.z = fmaf(x[j].z, f, acc.z);
+        acc.w = fmaf(x[j].w, f, acc.w);
+      }
+      if (!whole) {
+        *reinterpret_cast<float4*>(slot + r * D + d) = acc;
+        if (d == 0) *reinterpret_cast<float2*>(slot + kRows * D + 2 * r) = make_float2(mx, sum);
+      } else if (r < n_rows) {
+        write_row<D>(p, seq, it.head, group, row0 + r, d, acc, mx, sum);
+      }
+    }
+    if (!whole && it.item0 >= b_begin && threadIdx.x == 0)
+      p.desc[blockIdx.x] = make_int4(it.s, it.rt, it.head, static_cast<int>((it.item0 + it.steps - 1) / (quota * kWarps)));
+  }
 }
 
 // Joins the parts of a row tile that several blocks computed: block b holds its first
 // part (the end of b's run), blocks b + 1 .. last the others (the beginnings of theirs).
 template <int D, int NT>
-__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(256) attn_kv8_join_kernel(const AttnParams p) {
   using Cfg = AttnCfg<D, NT>;
   constexpr int kRows = Cfg::kRows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are still being computed
   const int4 item = p.desc[blockIdx.x];
   if (item.x < 0) return;
   const Kv8Args& a = p.a;
@@ -682,29 +726,41 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const AttnParams p) 
   auto part = [&](int i) {
     return base + (static_cast<int64_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * Cfg::kSlotFloats;
   };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < n_rows; r += 4) {
+  constexpr int kVec = D / 4;
+  const int lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < kRows * kVec; e += 256) {
+    const int r = e / kVec, d = 4 * (e % kVec);
+    // the lanes of a row look at its parts' maxima together
     float mx = -INFINITY;
-    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, part(i)[kRows * D + 2 * r]);
+    for (int i = lane % kVec; i < parts; i += kVec) mx = fmaxf(mx, part(i)[kRows * D + 2 * r]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    float sum = 0.0f, acc[D / 32];
+    for (int o = kVec / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    float sum = 0.0f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAhead = 8;
+    for (int i0 = 0; i0 < parts; i0 += kAhead) {
+      float2 ml[kAhead];
+      float4 x[kAhead];
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) acc[d] = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-      const float* q = part(i);
-      const float pm = q[kRows * D + 2 * r];
-      const float f = pm == -INFINITY ? 0.0f : ex2(pm - mx);
-      sum = fmaf(q[kRows * D + 2 * r + 1], f, sum);
+      for (int j = 0; j < kAhead; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.0f);
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + j < parts) {
+          ml[j] = *reinterpret_cast<const float2*>(part(i0 + j) + kRows * D + 2 * r);
+          x[j] = *reinterpret_cast<const float4*>(part(i0 + j) + r * D + d);
+        }
+      }
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(q[r * D + 32 * d + lane], f, acc[d]);
+      for (int j = 0; j < kAhead; ++j) {
+        const float f = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - mx);
+        sum = fmaf(ml[j].y, f, sum);
+        acc.x = fmaf(x[j].x, f, acc.x);
+        acc.y = fmaf(x[j].y, f, acc.y);
+        acc.z = fmaf(x[j].z, f, acc.z);
+        acc.w = fmaf(x[j].w, f, acc.w);
+      }
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const int rr = row0 + r, tok = rr / group;
-    const int64_t o = static_cast<int64_t>(seq.first + tok) * a.n_heads + item.z * group + (rr - tok * group);
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) p.out[o * D + 32 * d + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[d] * inv));
-    if (p.lse && lane == 0) p.lse[o] = sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    if (r < n_rows) write_row<D>(p, seq, item.z, group, row0 + r, d, acc, mx, sum);
   }
 }
 
@@ -718,10 +774,11 @@ template <int D, int NT>
 cudaError_t launch(AttnParams p, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, cudaStream_t stream) {
   using Cfg = AttnCfg<D, NT>;
   const int blocks = num_sms() * Cfg::kBlocksPerSm;
-  const int smem = Cfg::kRingBytes + Cfg::kJoinBytes + static_cast<int>(sizeof(AttnCtl)) + (p.a.S + 1) * 4 + 1024;
-  static_assert(Cfg::kRingBytes + Cfg::kJoinBytes + sizeof(AttnCtl) + (kKv8MaxSeqs + 1) * 4 + 1024 <= 227 * 1024, "shared memory per block");
+  const int smem = Cfg::kRingBytes + static_cast<int>(sizeof(AttnCtl)) + (p.a.S + 1) * 4 + 1024;
+  static_assert(Cfg::kRingBytes + sizeof(AttnCtl) + (kKv8MaxSeqs + 1) * 4 + 1024 <= 227 * 1024, "shared memory per block");
   p.desc = static_cast<int4*>(workspace);
   p.slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16 * static_cast<size_t>(blocks));
+  p.warp_slots = p.slots + static_cast<size_t>(blocks) * 2 * Cfg::kSlotFloats;
   auto kern = attn_kv8_kernel<D, NT>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), 227 * 1024, allowed);
@@ -731,22 +788,35 @@ cudaError_t launch(AttnParams p, const CUtensorMap& tmK, const CUtensorMap& tmV,
     kern<<<blocks, Cfg::kThreads, smem, stream>>>(tmK, tmV, p);
   }
   e = cudaGetLastError();
-  // no item has two units when a sequence cannot pass one: nothing to join
-  if (e != cudaSuccess || static_cast<int64_t>(p.a.max_pages) * p.a.page <= Cfg::kUnit) return e;
-  {
-    LaunchScope scope(stream, "attn_kv8_join_kernel");
-    attn_kv8_join_kernel<D, NT><<<blocks, 128, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  // no item is longer than a block's run when a sequence cannot pass one step: nothing to join
+  if (e != cudaSuccess || static_cast<int64_t>(p.a.max_pages) * p.a.page <= Cfg::kTile) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the kernel before it
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  LaunchScope scope(stream, "attn_kv8_join_kernel");
+  e = cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<D, NT>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D, int NT>
 size_t workspace_of() {
   using Cfg = AttnCfg<D, NT>;
-  return static_cast<size_t>(num_sms()) * Cfg::kBlocksPerSm * (16 + 2 * Cfg::kSlotFloats * 4);
+  return static_cast<size_t>(num_sms()) * Cfg::kBlocksPerSm * (16 + 2 * Cfg::kSlotFloats * 4 * (1 + Cfg::kWarps));
 }
 
 }  // namespace
+
+double attn_kv8_steps(const Kv8Args& a) {
+  const int nt = tiles_of(a);
+  const double tiles = static_cast<double>(a.T) * (a.n_heads / a.n_kv) / (8 * nt) + a.S;
+  return tiles * a.n_kv * (static_cast<double>(a.max_pages) * a.page / (nt == 4 ? kBox : 2 * kBox) + 1.0);
+}
 
 size_t attn_kv8_workspace(const Kv8Args& a) {
   const int nt = tiles_of(a);
