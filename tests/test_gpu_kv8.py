@@ -234,7 +234,7 @@ def _check_keys(c, gpu, keys, qkv):
         assert (np.abs(got - new) <= np.maximum(2.0 ** -4 * np.abs(new), 2.0 ** -10 * scale) * (1 + 2.0 ** -20) + err).all()
 
 
-@pytest.mark.parametrize("n_heads,n_kv,d", [(8, 8, 128), (8, 2, 64), (14, 2, 128), (5, 1, 64)])
+@pytest.mark.parametrize("n_heads,n_kv,d", [(6, 6, 128), (8, 2, 64), (14, 2, 128), (5, 1, 64)])
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
 def test_append(ar, n_heads, n_kv, d, page):
     """From one token to several pages a sequence, pages begun before (whose scale grows, or does not), none, far
@@ -251,7 +251,7 @@ def test_append(ar, n_heads, n_kv, d, page):
     gpu = c.gpu()
     q_out = torch.full((T, n_heads * d), 7.0, dtype=torch.bfloat16, device="cuda")
     ar.ar_kv8_append(qkv, cud, ld, torch.from_numpy(c.table).cuda(), *gpu, q_out, 2 * page + 7)
-    assert ar.ar_get_device_status() == ar.AR_OK
+    assert ar.ar_get_device_status() == ar.AR_OK, ar.ar_last_error()
     before = c.k.copy()
     rq, keys = L.kv8_append(qkv.double().cpu().numpy()[:cu[-1]], cu, lens, c.table, c.k, c.v, c.ks, c.vs, n_heads)
     got = q_out[:cu[-1]].double().cpu().numpy().reshape(rq.shape)
