@@ -212,8 +212,8 @@ cudaError_t launch_fold_mxfp4(const float* dW, const uint16_t* W, float* V, floa
                               cudaStream_t stream);
 cudaError_t launch_expand_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t n, uint16_t* out,
                                 cudaStream_t stream);
-// MXFP4 weights (E2M1 codes uint8 [N][K/2], E8M0 scales uint8 [N][K/32]), any T, K % 32 == 0: the tcgen05
-// dequant GEMM (ar_w4a16_tc.cu)
+// MXFP4 weights (E2M1 codes uint8 [N][K/2], E8M0 scales uint8 [N][K/32]), any T, K % 32 == 0: a tcgen05
+// GEMM that expands them (ar_mxfp4_tc.cu)
 cudaError_t launch_mxfp4_tc(const uint16_t* A, int T, const uint8_t* codes, const uint8_t* scales, int N, int K,
                             uint16_t* out, cudaStream_t stream);
 // ---- the paged 8-bit cache (ar_kv8.cu, ar_attn_kv8.cu) ----

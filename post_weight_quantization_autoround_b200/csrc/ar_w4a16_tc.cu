@@ -85,7 +85,7 @@ __host__ __device__ constexpr bool slot_phases_in_order(int per_slot, int sets, 
   return per_slot % sets == 0 || (sets % per_slot == 0 && slots % (sets / per_slot) == 0);
 }
 
-template <int TN, int BITS, int FP4 = 0>
+template <int TN, int BITS, bool FP4 = false>
 struct TcCfg {
   // One dequantization warp per TMEM lane quarter is latency bound (its nibble
   // and permute chains), so narrow tiles, whose epilogue needs few registers,
@@ -139,8 +139,7 @@ struct TcCtl {
 struct TcParams {
   const uint16_t* s16;  // fp16 bits [N][G]
   const uint16_t* z16;
-  const uint8_t* sc8;   // NVFP4: E4M3 block-scale codes [N][K/16]; MXFP4: E8M0 codes [N][blocks]
-  int blocks;           // MXFP4: blocks of 32 in a row (K rounds the row up to whole stages)
+  const uint8_t* sc8;   // NVFP4: E4M3 block-scale codes [N][K/16]
   const float* gscale;  // NVFP4: device per-tensor scale S
   uint16_t* out;        // bf16 bits [T][N]
   int N, K, T, G;
@@ -265,11 +264,6 @@ __device__ __forceinline__ void dequant4b(uint32_t x, float zf, uint32_t* o) {
   o[1] = pack_bf16x2(f[2], f[3]);
 }
 
-// The values of the FP4 template parameter: integer codes, or E2M1 codes with
-// NVFP4's block scales (E4M3 per 16, one per-tensor scale) or MXFP4's (E8M0 per 32).
-constexpr int kNvFp4 = 1;
-constexpr int kMxFp4 = 2;
-
 // 8 E2M1 codes of one word (element k in bits 4k..4k+3; code = sign << 3 |
 // magnitude index) -> 8 bf16 values in k order, each times the bf16 pair sc2 (the
 // block scale in both halves).  The magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 are
@@ -278,7 +272,7 @@ constexpr int kMxFp4 = 2;
 // through byte permutes, give four values per permute; the sign bit of each
 // code moves to bit 15 or 31 of its pair.  An E2M1 value times an E4M3 scale
 // has at most 6 significant bits and stays in bf16's normal range, so every
-// product is exact; so it is with a power of two (MXFP4).
+// product is exact.
 __device__ __forceinline__ uint4 dequant_e2m1x8(uint32_t x, uint32_t sc2) {
   constexpr uint32_t kL0 = 0xC0800000u, kL1 = 0xC0804000u;  // low bytes for magnitudes 0..3, 4..7
   constexpr uint32_t kH0 = 0x3F3F3F00u, kH1 = 0x40404040u;  // high bytes
@@ -317,12 +311,6 @@ __device__ __forceinline__ void e4m3x8_to_bf16_pairs(uint2 c, uint32_t (&sc2)[8]
       sc2[4 * h + 2 * i + 1] = pack_bf16x2(f1, f1);
     }
   }
-}
-
-// An E8M0 scale code as a bf16 pair (the scale in both halves): 2^(code - 127), 255 is NaN.
-__device__ __forceinline__ uint32_t e8m0_pair(uint32_t code) {
-  const uint32_t b = code == 0u ? 0x0040u : code == 255u ? 0x7FC0u : code << 7;
-  return b * 0x00010001u;
 }
 
 __device__ __forceinline__ uint32_t zero_pair(uint16_t z16) {
@@ -390,10 +378,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 
 // Grid: one CTA per (128-row tile, token tile, K half when split); the CTAs of
 // a weight tile are adjacent so that its codes come from HBM once.
-// FP4: NVFP4 or MXFP4 weights (E2M1 codes in the 4-bit layout, block scales folded
-// into the dequantized operand, NVFP4's per-tensor scale applied per group in the
+// FP4: NVFP4 weights (E2M1 codes in the 4-bit layout, E4M3 block scales folded
+// into the dequantized operand, the per-tensor scale applied per group in the
 // epilogue); BITS is then 4.
-template <int TN, int KSPLIT, int BITS, int FP4>
+template <int TN, int KSPLIT, int BITS, bool FP4>
 __global__ void __launch_bounds__(TcCfg<TN, BITS, FP4>::kThreads, 1)
     w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                     const TcParams p) {
@@ -633,24 +621,9 @@ __global__ void __launch_bounds__(TcCfg<TN, BITS, FP4>::kThreads, 1)
         const uint32_t qvv = qv + v;
         pw[v] = ld_shared_v4(pk + (qvv >> 3) * kCodeBytes + (((qvv & 7) ^ sw) << 4));
       }
-      // NVFP4: the row's 8 block scales of this stage (one per two words); MXFP4: its 4
-      // (one per four words; past the row's end the codes are zeros and any scale will do)
+      // NVFP4: the row's 8 block scales of this stage (one per two words)
       uint32_t sc2[8];
-      if constexpr (FP4 == kMxFp4) {
-        const int b0 = k0 / 32;
-        const uint8_t* row = p.sc8 + static_cast<size_t>(n < p.N ? n : 0) * p.blocks;
-        uint32_t c4 = 0x7F7F7F7Fu;
-        if (p.vec_meta) {
-          c4 = __ldg(reinterpret_cast<const uint32_t*>(row + b0));
-        } else {
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (b0 + b < p.blocks) c4 = (c4 & ~(0xFFu << (8 * b))) | (static_cast<uint32_t>(__ldg(row + b0 + b)) << (8 * b));
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) sc2[b] = e8m0_pair((c4 >> (8 * b)) & 0xFFu);
-      }
-      if constexpr (FP4 == kNvFp4) {
+      if (FP4) {
         uint2 c8 = make_uint2(0u, 0u);
         if (n < p.N) c8 = __ldg(reinterpret_cast<const uint2*>(p.sc8 + static_cast<size_t>(n) * (p.K / 16) + k0 / 16));
         e4m3x8_to_bf16_pairs(c8, sc2);
@@ -700,7 +673,7 @@ __global__ void __launch_bounds__(TcCfg<TN, BITS, FP4>::kThreads, 1)
             const int quarter = w / BITS;
             const int col = (w - half * 2 * BITS) * (16 / BITS);  // first column of this word in the half
             if (FP4) {
-              const uint4 o = dequant_e2m1x8(xs[u], sc2[FP4 == kMxFp4 ? w >> 2 : w >> 1]);  // word w holds k 8w .. 8w + 7
+              const uint4 o = dequant_e2m1x8(xs[u], sc2[w >> 1]);  // word w holds k 8w .. 8w + 7: block w / 2
               a[col] = o.x;
               a[col + 1] = o.y;
               a[col + 2] = o.z;
@@ -740,7 +713,7 @@ __global__ void __launch_bounds__(TcCfg<TN, BITS, FP4>::kThreads, 1)
     constexpr int gstep = Cfg::kGrpSplit;
     MetaRow srow;
     if (!FP4) srow.start(p.s16 + static_cast<size_t>(n < p.N ? n : 0) * p.G, g_begin + gfirst, p.G, p.vec_meta != 0, n < p.N);
-    const float S = FP4 == kNvFp4 ? __ldg(p.gscale) : 1.f;  // MXFP4 has no per-tensor scale
+    const float S = FP4 ? __ldg(p.gscale) : 0.f;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
     for (int li = gfirst; li < n_groups; li += gstep) {
       const uint32_t buf = static_cast<uint32_t>(li % Cfg::kNBuf);
@@ -806,13 +779,13 @@ __global__ void __launch_bounds__(TcCfg<TN, BITS, FP4>::kThreads, 1)
   }
 }
 
-template <int TN, int KSPLIT, int BITS, int FP4>
+template <int TN, int KSPLIT, int BITS, bool FP4>
 cudaError_t launch_tc(const uint16_t* A, const CUtensorMap& tmW, TcParams p, int n_tiles, cudaStream_t stream,
-                      const char* name, int act_k) {
+                      const char* name) {
   using Cfg = TcCfg<TN, BITS, FP4>;
   CUtensorMap tmA;
   cudaError_t e = make_tmap_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, static_cast<uint64_t>(p.T),
-                               static_cast<uint64_t>(act_k), 64, TN, CU_TENSOR_MAP_SWIZZLE_128B);  // kSub boxes per stage
+                               static_cast<uint64_t>(p.K), 64, TN, CU_TENSOR_MAP_SWIZZLE_128B);  // kSub boxes per stage
   if (e != cudaSuccess) return e;
   constexpr int smem = Cfg::kRingBytes + static_cast<int>(sizeof(TcCtl)) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
@@ -837,22 +810,21 @@ cudaError_t launch_tc(const uint16_t* A, const CUtensorMap& tmW, TcParams p, int
   return cudaGetLastError();
 }
 
-template <int TN, int BITS, int FP4 = 0>
+template <int TN, int BITS, bool FP4 = false>
 cudaError_t launch_tn(const uint16_t* A, const CUtensorMap& tmW, TcParams p, int n_tiles, cudaStream_t stream,
-                      const char* name1, const char* name2, int act_k = 0) {
-  if (act_k == 0) act_k = p.K;  // values in a row of activations
+                      const char* name1, const char* name2) {
   // Split K over a CTA pair when one CTA per tile leaves more than half the SMs idle.
   const int tiles = n_tiles * p.t_tiles;
   const int total_units = p.K / p.unit_k;
   if (2 * tiles <= num_sms() && total_units >= 2) {
     p.split_units = (total_units + 1) / 2;
     const int g_split = (p.split_units * p.unit_k) >> p.group_shift;
-    p.vec_meta = FP4 == kMxFp4 ? p.blocks % 4 == 0 : (p.G % 8 == 0 && g_split % 8 == 0) ? 1 : 0;
-    return launch_tc<TN, 2, BITS, FP4>(A, tmW, p, n_tiles, stream, name2, act_k);
+    p.vec_meta = (p.G % 8 == 0 && g_split % 8 == 0) ? 1 : 0;
+    return launch_tc<TN, 2, BITS, FP4>(A, tmW, p, n_tiles, stream, name2);
   }
   p.split_units = total_units;
-  p.vec_meta = FP4 == kMxFp4 ? p.blocks % 4 == 0 : p.G % 8 == 0 ? 1 : 0;
-  return launch_tc<TN, 1, BITS, FP4>(A, tmW, p, n_tiles, stream, name1, act_k);
+  p.vec_meta = p.G % 8 == 0 ? 1 : 0;
+  return launch_tc<TN, 1, BITS, FP4>(A, tmW, p, n_tiles, stream, name1);
 }
 
 
@@ -893,11 +865,6 @@ constexpr const char* kFp4Names[8] = {"nvfp4_tc_kernel<TN=16>", "nvfp4_tc_kernel
                                       "nvfp4_tc_kernel<TN=32>", "nvfp4_tc_kernel<TN=32,split2>",
                                       "nvfp4_tc_kernel<TN=64>", "nvfp4_tc_kernel<TN=64,split2>",
                                       "nvfp4_tc_kernel<TN=128>", "nvfp4_tc_kernel<TN=128,split2>"};
-
-constexpr const char* kMxNames[8] = {"mxfp4_tc_kernel<TN=16>", "mxfp4_tc_kernel<TN=16,split2>",
-                                     "mxfp4_tc_kernel<TN=32>", "mxfp4_tc_kernel<TN=32,split2>",
-                                     "mxfp4_tc_kernel<TN=64>", "mxfp4_tc_kernel<TN=64,split2>",
-                                     "mxfp4_tc_kernel<TN=128>", "mxfp4_tc_kernel<TN=128,split2>"};
 
 template <int BITS>
 cudaError_t launch_bits_tc(const uint16_t* A, int T, const uint32_t* packed, const uint16_t* scale16,
@@ -963,46 +930,18 @@ cudaError_t launch_nvfp4_tc(const uint16_t* A, int T, const uint8_t* codes, cons
   const int n_tiles = (N + kTcRows - 1) / kTcRows;
   if (T <= 16) {
     p.t_tiles = 1;
-    return launch_tn<16, 4, kNvFp4>(A, tmW, p, n_tiles, stream, kFp4Names[0], kFp4Names[1]);
+    return launch_tn<16, 4, true>(A, tmW, p, n_tiles, stream, kFp4Names[0], kFp4Names[1]);
   }
   if (T <= 32) {
     p.t_tiles = 1;
-    return launch_tn<32, 4, kNvFp4>(A, tmW, p, n_tiles, stream, kFp4Names[2], kFp4Names[3]);
+    return launch_tn<32, 4, true>(A, tmW, p, n_tiles, stream, kFp4Names[2], kFp4Names[3]);
   }
   if (T <= 64) {
     p.t_tiles = 1;
-    return launch_tn<64, 4, kNvFp4>(A, tmW, p, n_tiles, stream, kFp4Names[4], kFp4Names[5]);
+    return launch_tn<64, 4, true>(A, tmW, p, n_tiles, stream, kFp4Names[4], kFp4Names[5]);
   }
   p.t_tiles = (T + 127) / 128;
-  return launch_tn<128, 4, kNvFp4>(A, tmW, p, n_tiles, stream, kFp4Names[6], kFp4Names[7]);
-}
-
-cudaError_t launch_mxfp4_tc(const uint16_t* A, int T, const uint8_t* codes, const uint8_t* scales, int N, int K,
-                            uint16_t* out, cudaStream_t stream) {
-  if (T < 1 || N < 1 || K < 32 || K % 32 != 0) return cudaErrorInvalidValue;
-  TcParams p{};
-  p.sc8 = scales;
-  p.out = out;
-  p.N = N;
-  p.K = (K + kTcK - 1) / kTcK * kTcK;  // the copies fill what lies past the rows with zeros
-  p.T = T;
-  p.blocks = K / 32;
-  // accumulation groups as for NVFP4: no scale differs between them
-  p.group_shift = 7;
-  while (p.group_shift < 10 && p.K % (1 << (p.group_shift + 1)) == 0) ++p.group_shift;
-  p.G = p.K >> p.group_shift;
-  p.unit_k = 1 << p.group_shift;
-  CUtensorMap tmW;
-  cudaError_t e = make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, codes, static_cast<uint64_t>(N),
-                               static_cast<uint64_t>(K) / 8, 32, kTcRows, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e != cudaSuccess) return e;
-  const int n_tiles = (N + kTcRows - 1) / kTcRows;
-  p.t_tiles = 1;
-  if (T <= 16) return launch_tn<16, 4, kMxFp4>(A, tmW, p, n_tiles, stream, kMxNames[0], kMxNames[1], K);
-  if (T <= 32) return launch_tn<32, 4, kMxFp4>(A, tmW, p, n_tiles, stream, kMxNames[2], kMxNames[3], K);
-  if (T <= 64) return launch_tn<64, 4, kMxFp4>(A, tmW, p, n_tiles, stream, kMxNames[4], kMxNames[5], K);
-  p.t_tiles = (T + 127) / 128;
-  return launch_tn<128, 4, kMxFp4>(A, tmW, p, n_tiles, stream, kMxNames[6], kMxNames[7], K);
+  return launch_tn<128, 4, true>(A, tmW, p, n_tiles, stream, kFp4Names[6], kFp4Names[7]);
 }
 
 cudaError_t launch_wxa16_tc(const uint16_t* A, int T, const uint32_t* packed, const uint16_t* scale16,
