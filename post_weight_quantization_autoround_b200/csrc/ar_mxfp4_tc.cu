@@ -8,7 +8,7 @@
 //  * One CTA owns 128 weight rows (the MMA's M) and up to 256 tokens (its N): the expansion of
 //    a weight serves 256 tokens, and at N = 256 the MMAs of a 64-k stage take 512 cycles, longer
 //    than its expansion (at N = 128 the two are even).
-//  * Eight warps expand (two sets on alternating stages, a warp per 32 TMEM lanes): the codes
+//  * Sixteen warps expand (four sets in turn, each a stage; with two the chains of one warp set the pace, a warp per 32 TMEM lanes): the codes
 //    of a stage are 32 bytes a row in shared memory (TMA, 128-byte swizzle), and the bf16 tile
 //    goes straight to tensor memory as the MMA's A operand.  A code's sign and its three other
 //    bits, moved to the sign and to the two lowest exponent bits and highest mantissa bit of a
@@ -30,8 +30,8 @@ constexpr int kSlots = 4;                    // code boxes: 128 rows x 256 k, 4 
 constexpr int kSlotBytes = kRows * 128;
 constexpr int kStagesPerSlot = 4;
 constexpr int kACols = kStageK / 2;
-constexpr int kFirstWorker = 4;              // warps: activation TMA, MMA, code TMA, idle, 8 workers
-constexpr int kWorkers = 8;
+constexpr int kFirstWorker = 4;              // warps: activation TMA, MMA, code TMA, idle, 16 workers
+constexpr int kWorkers = 16;
 constexpr int kSets = kWorkers / 4;
 constexpr int kThreads = (kFirstWorker + kWorkers) * 32;
 
@@ -297,8 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kFirstWorker) {
     const int set = (warp - kFirstWorker) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-#pragma unroll
-    for (int c = set * (TN / kSets); c < (set + 1) * (TN / kSets); c += 16) {
+    constexpr int kEpSets = TN / 16 < kSets ? TN / 16 : kSets;  // sets that read: 16 columns at a time
+    constexpr int kEpCols = TN / kEpSets;
+#pragma unroll 1
+    for (int c = set * kEpCols; set < kEpSets && c < (set + 1) * kEpCols; c += 16) {
       uint32_t v[16];
       asm volatile(
           "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
