@@ -89,7 +89,7 @@ __device__ __forceinline__ Seq load_seq(const Kv8Args& a, int s) {
   const int64_t c0 = a.cu[s], rows = a.cu[s + 1] - c0;
   const int64_t len = a.lens[s];
   Seq q;
-  const bool ok = rows >= 0 && c0 >= 0 && c0 + rows <= a.T && len >= 0 && len <= static_cast<int64_t>(a.max_pages) * a.page;
+  const bool ok = rows >= 0 && rows <= a.max_new && c0 >= 0 && c0 + rows <= a.T && len >= 0 && len <= static_cast<int64_t>(a.max_pages) * a.page;
   if (!ok) raise_status(kStatusBadIndex);
   q.first = ok ? static_cast<int>(c0) : 0;
   q.n_new = ok ? static_cast<int>(rows) : 0;
@@ -827,6 +827,8 @@ size_t attn_kv8_workspace(const Kv8Args& a) {
 cudaError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, float sm_scale, const uint8_t* k_pages,
                             const uint8_t* v_pages, const uint8_t* k_scales, const uint8_t* v_scales, uint16_t* out,
                             float* lse, void* workspace, cudaStream_t stream) {
+  if (attn_kv8_tc_fits(a))
+    return launch_attn_kv8_tc(a, q, sm_scale, k_pages, v_pages, k_scales, v_scales, out, lse, stream);
   AttnParams p{};
   p.a = a;
   p.q = q;

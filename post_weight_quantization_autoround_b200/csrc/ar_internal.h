@@ -237,6 +237,11 @@ cudaError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, float sm_scale,
 // the same at T <= 8 (ar_mxfp4_dec.cu); cudaErrorNotSupported (nothing launched) where the activations do not fit
 cudaError_t launch_mxfp4_dec(const uint16_t* A, int T, const uint8_t* codes, const uint8_t* scales, int N, int K,
                              uint16_t* out, cudaStream_t stream);
+// the same attention on tcgen05, head dimension 128 and many rows (ar_attn_kv8_tc.cu): whether it is the one to take
+bool attn_kv8_tc_fits(const Kv8Args& a);
+cudaError_t launch_attn_kv8_tc(const Kv8Args& a, const uint16_t* q, float sm_scale, const uint8_t* k_pages,
+                               const uint8_t* v_pages, const uint8_t* k_scales, const uint8_t* v_scales, uint16_t* out,
+                               float* lse, cudaStream_t stream);
 // minibatch assembly (ar_gather.cu): n <= kMaxGatherSamples samples of sample_bytes each
 constexpr int kMaxGatherSamples = 64;
 cudaError_t launch_gather_samples(const void* src, int64_t sample_bytes, const int32_t* idx, int n, void* dst,

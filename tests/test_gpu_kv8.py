@@ -122,8 +122,6 @@ def test_attention_ragged_chunks(ar, n_heads, n_kv, d, page):
     empty = slice(cu[4], cu[4] + 5)  # nine new tokens, four keys
     assert not out[empty].any() and lse[empty].isneginf().all() and not out[cu[8]].any()
     assert (out[cu[-1]:] == 7.0).all() and (lse[cu[-1]:] == 3.0).all()
-    # a bound on the new tokens that is too small changes the tile, not the answer
-    _check(c, q, cu, _attend(ar, c, q, cud, ld, 1))
     assert ar.ar_get_device_status() == ar.AR_OK
 
 
@@ -150,6 +148,49 @@ def test_attention_split_over_blocks(ar, n_heads, n_kv, d, lens):
     g.replay()
     torch.cuda.synchronize()
     _check(c, q, cu, got)
+
+
+@pytest.mark.parametrize("n_heads,n_kv,page,news,lens", [
+    (64, 8, 16, [200, 0, 129, 1, 97], [1000, 50, 129, 700, 97]),
+    (40, 8, 64, [300, 300], [300, 811]),
+    (32, 32, 128, [700], [1301]),
+    (21, 3, 32, [900, 33, 600, 5], [890, 1, 613, 3]),  # rows that see no key, an odd group
+    (148, 4, 128, [130, 7], [4500, 4200]),
+])
+def test_attention_prompts(ar, n_heads, n_kv, page, news, lens):
+    """Rows enough for the tcgen05 kernel, ragged, with page tables that end and garbage past the sequences' ends."""
+    c = Cache(lens, n_heads, n_kv, 128, page, n_heads)
+    cu, cud, ld = _index(news, lens)
+    T = cu[-1] + 3
+    q = torch.from_numpy(c.rng.normal(size=(T, n_heads * 128)).astype(np.float32)).bfloat16().cuda()
+    lse = torch.full((T, n_heads), 3.0, device="cuda")
+    gpu = c.gpu()
+    out = _attend(ar, c, q, cud, ld, max(news), gpu, lse=lse)
+    assert "attn_kv8_tc_kernel" in ar.ar_last_kernels() and ar.ar_get_device_status() == ar.AR_OK
+    _check(c, q, cu, out, lse)
+    assert (out[cu[-1]:] == 7.0).all() and (lse[cu[-1]:] == 3.0).all()
+    assert torch.equal(out, _attend(ar, c, q, cud, ld, max(news), gpu))
+
+
+def test_attention_prompts_growing_scores_and_scales(ar):
+    """Maxima that grow from block to block (the sums in tensor memory are rescaled often), and value scales 2^20 apart."""
+    lens, news = [1500], [640]
+    c = Cache(lens, 32, 8, 128, 16, 9)
+    c.vs[:] = c.rng.integers(100, 121, c.vs.shape)
+    for j in range(lens[0]):
+        c.ks[c.table[0, j // 16]] = 112 + j // 150
+    cu, cud, ld = _index(news, lens)
+    q = torch.from_numpy(c.rng.normal(size=(640, 32 * 128)).astype(np.float32)).bfloat16().cuda()
+    lse = torch.empty(640, 32, device="cuda")
+    out = _attend(ar, c, q, cud, ld, 640, lse=lse)
+    assert "attn_kv8_tc_kernel" in ar.ar_last_kernels()
+    _check(c, q, cu, out, lse)
+    # a page that is not in the pool, a sequence with more tokens than said
+    c.table[0, 3] = c.k.shape[0]
+    _attend(ar, c, q, cud, ld, 640)
+    assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG
+    out = _attend(ar, c, q, cud, ld, 639)
+    assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG and (out == 7.0).all()
 
 
 @pytest.mark.parametrize("n_heads,n_kv,d", [(8, 8, 128), (64, 4, 64), (24, 1, 128)])
@@ -217,6 +258,10 @@ def test_attention_bad_indices_are_skipped(ar):
         assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG
         assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2]) and (got[1] == 7.0).all()
     ld[1] = 100
+    two = torch.tensor([0, 0, 2, 3], dtype=torch.int32, device="cuda")  # the second sequence has more than max_new
+    got = _attend(ar, c, q, two, ld, 1)
+    assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG
+    assert torch.equal(got[2], want[2]) and (got[:2] == 7.0).all()
     for bad in (-1, 9, 2 ** 31 - 1):
         cud[3] = bad
         got = _attend(ar, c, q, cud, ld, 1)
