@@ -8,11 +8,11 @@
 // blocks of 128 keys.  Warp roles:
 //  * 0: tensor memory; one lane issues S = Q K^T (M = 128 rows, N = 128 keys, K = 128).
 //  * 1: one lane issues O += P V (A = P as f16 pairs in tensor memory, B = V MN-major).
-//  * 2-9: softmax.  Warp w reads TMEM lanes 32 (w % 4) .. (a row a thread) and half of the block's
-//    keys; the two warps of a row exchange their maxima through shared memory (a bounded barrier).
+//  * 2-17: softmax.  Warp w reads TMEM lanes 32 (w % 4) .. (a row a thread) and a quarter of the block's
+//    keys; the four warps of a row exchange their maxima through shared memory (a bounded barrier).
 //    The reference m only moves when a block's maximum passes it by 2^8, which f16 holds with room:
 //    O is then rescaled in tensor memory, which almost no block needs after the first.
-//  * 10-17: expansion.  Codes come straight from the pages to registers a block ahead, each
+//  * 18-25: expansion.  Codes come straight from the pages to registers a block ahead, each
 //    conversion instruction makes two f16, and the tile is written as the MMAs read it (128-byte
 //    swizzle; the same layout serves K as the K-major and V as the MN-major operand).
 //
@@ -28,13 +28,15 @@ constexpr int kD = 128;
 constexpr int kBlk = 128;                 // rows of a tile, keys of a block
 constexpr int kBox = kBlk * 128;          // 128 rows x 64 f16
 constexpr int kTile = 2 * kBox;
-constexpr int kSmWarps = 8;
+constexpr int kSmWarps = 16;
+constexpr int kPerQ = kSmWarps / 4;       // softmax warps of a row
 constexpr int kSmWarp0 = 2;
 constexpr int kExWarps = 8;
 constexpr int kExWarp0 = kSmWarp0 + kSmWarps;
 constexpr int kExThreads = kExWarps * 32;
 constexpr int kThreads = (kExWarp0 + kExWarps) * 32;
-constexpr int kCols = kBlk / 2;           // keys of a softmax warp
+constexpr int kCols = kBlk / kPerQ;       // keys of a block, and columns of O, of a softmax warp
+static_assert(kCols == 32, "a softmax warp loads and stores 32-column slices");
 constexpr int kGroups = kCols / 16;       // of 16 tokens: one scale each
 constexpr uint32_t kColS = 0, kColP = 256, kColO = 384;
 constexpr float kSlack = 8.0f;            // a block's maximum may pass the reference by 2^8
@@ -44,11 +46,11 @@ struct Ctl {
   uint64_t q_full;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
-  uint64_t ex_full[4][2];                 // maxima of a lane quarter's two warps
+  uint64_t ex_full[4][2];                 // maxima of a lane quarter's warps
   uint64_t o_full, done_s, done_pv;
   uint32_t tmem_base;
   int abort_flag;
-  float ex[2][4][2][32];                  // [block parity][quarter][half][row]
+  float ex[2][4][kPerQ][32];              // [block parity][quarter][part][row]
   float fac[kBlk];                        // a row's factor to log2 units
 };
 
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       mbar_init(&ctl->s_empty[i], kSmWarps);
       mbar_init(&ctl->p_full[i], kSmWarps);
       mbar_init(&ctl->p_empty[i], 1);
-      for (int q = 0; q < 4; ++q) mbar_init(&ctl->ex_full[q][i], 2);
+      for (int q = 0; q < 4; ++q) mbar_init(&ctl->ex_full[q][i], kPerQ);
     }
     mbar_init(&ctl->o_full, 1);
     mbar_init(&ctl->done_s, 1);
@@ -205,10 +207,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
     }
   } else if (warp < kExWarp0) {
     // ------------------------------------------------------------ softmax and output
-    const int quarter = warp & 3, half = (warp - kSmWarp0) >> 2;
+    const int quarter = warp & 3, sub = (warp - kSmWarp0) >> 2;
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int k0 = half * kCols;
+    const int k0 = sub * kCols;
     const int rr = row0 + r;
     const int lim = rr < n_rows ? start + rr / group + 1 : 0;  // keys the row sees
     // lane i < kGroups looks up group i of a block: page two blocks ahead, scale codes one block ahead
@@ -234,9 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->s_full[b], par, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      float u[2][32];
-      tmem_ld32(tmem + lane_off + kColS + b * kBlk + k0, u[0]);
-      tmem_ld32(tmem + lane_off + kColS + b * kBlk + k0 + 32, u[1]);
+      float x[kCols];
+      tmem_ld32(tmem + lane_off + kColS + b * kBlk + k0, x);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->s_empty[b]);
@@ -250,8 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
         const float f = fac * __uint_as_float(max(min(ek, 254u), 1u) << 23);
         const float fe = static_cast<float>(static_cast<int>(ev) - 127);
         back[g] = __uint_as_float(max(254u - min(ev, 253u), 1u) << 23);  // 2^-ev
-        float(&x)[32] = u[g >> 1];
-        const int o = 16 * (g & 1);
+        const int o = 16 * g;
         const int end = e < 0 ? 0 : lim;  // a group whose page is not in the pool, or past the keys: nothing
         if (tb + 16 * g + 16 > full_below || e < 0) {
 #pragma unroll
@@ -269,14 +269,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
         top = fmaxf(top, fmaxf(t0, t1));
       }
       exps = exps_next;
-      // the row's maximum over both halves
-      ctl->ex[b][quarter][half][lane] = top;
+      // the row's maximum over all parts
+      ctl->ex[b][quarter][sub][lane] = top;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->ex_full[quarter][b]);
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->ex_full[quarter][b], par, abort_flag));
       if (!ok) break;
-      top = fmaxf(top, ctl->ex[b][quarter][half ^ 1][lane]);
-      // both warps of a row come to the same decision
+#pragma unroll
+      for (int i = 0; i < kPerQ; ++i) top = fmaxf(top, ctl->ex[b][quarter][i][lane]);
+      // all warps of a row come to the same decision
       const bool move = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
       if (__any_sync(0xFFFFFFFFu, move)) {
         const float to = move ? top : m;
@@ -284,48 +285,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
         l *= f;
         m = to;
         if (j > 0) {
-          // O holds the blocks before: wait for the last of their products, rescale this warp's 64 columns
+          // O holds the blocks before: wait for the last of their products, rescale this warp's 32 columns
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->p_empty[b ^ 1], static_cast<uint32_t>((j - 1) >> 1) & 1u, abort_flag));
           if (!ok) break;
           tc_fence_after();
+          float o[kCols];
+          tmem_ld32(tmem + lane_off + kColO + k0, o);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float o[32];
-            tmem_ld32(tmem + lane_off + kColO + half * 64 + 32 * h, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st32(tmem + lane_off + kColO + half * 64 + 32 * h, o);
-          }
+          for (int i = 0; i < kCols; ++i) o[i] *= f;
+          tmem_st32(tmem + lane_off + kColO + k0, o);
           at_tmem_st_wait();
         }
       }
       const float ref = m == -INFINITY ? 0.0f : m;
-      uint32_t pk[2][16];
+      uint32_t pk[kCols / 2];
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float p0 = at_ex2(u[g >> 1][16 * (g & 1) + 2 * i] - ref), p1 = at_ex2(u[g >> 1][16 * (g & 1) + 2 * i + 1] - ref);
+          const float p0 = at_ex2(x[16 * g + 2 * i] - ref), p1 = at_ex2(x[16 * g + 2 * i + 1] - ref);
           s0 += p0;
           s1 += p1;
-          pk[g >> 1][8 * (g & 1) + i] = pack_f16x2(p0, p1);
+          pk[8 * g + i] = pack_f16x2(p0, p1);
         }
         l = fmaf(s0 + s1, back[g], l);
       }
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->p_empty[b], par ^ 1u, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      at_tmem_st16(tmem + lane_off + kColP + b * 64 + k0 / 2, pk[0]);
-      at_tmem_st16(tmem + lane_off + kColP + b * 64 + k0 / 2 + 16, pk[1]);
+      at_tmem_st16(tmem + lane_off + kColP + b * 64 + k0 / 2, pk);
       at_tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->p_full[b]);
     }
-    // the row sum over both halves, through the same exchange (one phase further)
+    // the row sum over all parts, through the same exchange (one phase further), added in their order
     const int b = n_kb & 1;
-    ctl->ex[b][quarter][half][lane] = l;
+    ctl->ex[b][quarter][sub][lane] = l;
     __syncwarp();
     if (ok) {
       if (lane == 0) mbar_arrive(&ctl->ex_full[quarter][b]);
@@ -334,29 +331,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
     if (ok && n_kb > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->o_full, 0, abort_flag));
     if (ok) {
       tc_fence_after();
-      const float other = ctl->ex[b][quarter][half ^ 1][lane];
-      l = half == 0 ? l + other : other + l;
+      l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPerQ; ++i) l += ctl->ex[b][quarter][i][lane];
       const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
       const int tok = rr / group;
       const int64_t row = static_cast<int64_t>(first + tok) * a.n_heads + head * group + (rr - tok * group);
+      float o[kCols];
+      if (n_kb > 0) {
+        tmem_ld32(tmem + lane_off + kColO + k0, o);
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float o[32];
-        if (n_kb > 0) {
-          tmem_ld32(tmem + lane_off + kColO + half * 64 + 32 * h, o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-        }
-        if (rr < n_rows) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * kD + half * 64 + 32 * h);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-        }
+        for (int i = 0; i < kCols; ++i) o[i] = 0.0f;
       }
-      if (half == 0 && rr < n_rows && p.lse) p.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (rr < n_rows) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + row * kD + k0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dst[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                              pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        if (sub == 0 && p.lse) p.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
       tc_fence_before();
     }
   } else {
@@ -404,20 +399,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       }
     };
     bool bad = false;
-    int64_t at[kRowsPerThread];  // of the block being loaded, -1: nothing
+    int at[kRowsPerThread];  // row of the cache, of the block being loaded; -1: nothing
+    const uint32_t to_lo = chunk_at(t0, 2 * c16), to_hi = chunk_at(t0, 2 * c16 + 1);  // 32 rows further: 4096 bytes further
     auto places = [&](int j) {
 #pragma unroll
       for (int i = 0; i < kRowsPerThread; ++i) {
         const int t = j * kBlk + t0 + 32 * i;
         const bool in = pg[i] >= 0 && pg[i] < a.n_pages;
         bad |= t < keys && !in;
-        at[i] = in && t < keys ? ((static_cast<int64_t>(pg[i]) * a.n_kv + head) * a.page + (t & (a.page - 1))) * kD + c16 * 16 : -1;
+        at[i] = in ? (((pg[i] * a.n_kv + head) << p.page_shift) + (t & (a.page - 1))) : -1;
       }
     };
     auto load = [&](const uint8_t* src, uint4 (&w)[kRowsPerThread]) {
 #pragma unroll
       for (int i = 0; i < kRowsPerThread; ++i)
-        w[i] = at[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + at[i])) : make_uint4(0u, 0u, 0u, 0u);
+        w[i] = at[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + c16 * 16 + static_cast<int64_t>(at[i]) * kD)) : make_uint4(0u, 0u, 0u, 0u);
     };
     auto expand = [&](uint8_t* tile, const uint4 (&w)[kRowsPerThread]) {
 #pragma unroll
@@ -427,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
         e4m3x4_f16(w[i].y, lo.z, lo.w);
         e4m3x4_f16(w[i].z, hi.x, hi.y);
         e4m3x4_f16(w[i].w, hi.z, hi.w);
-        *reinterpret_cast<uint4*>(tile + chunk_at(t0 + 32 * i, 2 * c16)) = lo;
-        *reinterpret_cast<uint4*>(tile + chunk_at(t0 + 32 * i, 2 * c16 + 1)) = hi;
+        *reinterpret_cast<uint4*>(tile + to_lo + 4096 * i) = lo;
+        *reinterpret_cast<uint4*>(tile + to_hi + 4096 * i) = hi;
       }
       fence_async();
       __syncwarp();
