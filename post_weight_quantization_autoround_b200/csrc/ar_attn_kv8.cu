@@ -38,6 +38,8 @@ namespace {
 constexpr int kBox = 16;       // tokens of a copy: a page is a multiple of it
 constexpr int kChunk = 32;     // steps whose pages and scales the lanes hold
 constexpr int kMaxWarps = 8;
+// Steps one after another that a warp may be given so that no item leaves its block (see the launch function).
+constexpr int kFixedMax = 8;
 
 template <int D, int NT>
 struct AttnCfg {
@@ -78,6 +80,7 @@ struct AttnParams {
   float* warp_slots;  // [blocks][warps][2][kSlotFloats]
   int4* desc;    // [blocks]: {sequence, row tile, head, last block} of the item whose first part is the block's, or x = -1
   float scale_log2;
+  int fixed;     // steps that every item counts as, a multiple of the block's warps; 0: as many as it has
 };
 
 // a sequence's bounds, checked against the arrays
@@ -221,12 +224,14 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  // short caches: every item counts as many steps as the longest may have, and a block's run holds whole items
+  auto item_steps_of = [&](int keys) { return p.fixed > 0 ? p.fixed : steps_of<kTile>(keys); };
   // steps of every sequence: a thread each where it is one row tile, else a warp each
   if (a.max_new * group <= kRows) {
     for (int s = threadIdx.x; s < a.S; s += kThreads) {
       const Seq q = load_seq(a, s);
       uint32_t u = 0;
-      for (int rt = 0; rt < row_tiles(q, kRows, group); ++rt) u += steps_of<kTile>(tile_keys(q, rt, kRows, group));
+      for (int rt = 0; rt < row_tiles(q, kRows, group); ++rt) u += item_steps_of(tile_keys(q, rt, kRows, group));
       prefix[s + 1] = u * a.n_kv;
     }
   } else {
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
       const Seq q = load_seq(a, s);
       const int nrt = row_tiles(q, kRows, group);
       uint32_t u = 0;
-      for (int rt = lane; rt < nrt; rt += 32) u += steps_of<kTile>(tile_keys(q, rt, kRows, group));
+      for (int rt = lane; rt < nrt; rt += 32) u += item_steps_of(tile_keys(q, rt, kRows, group));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
       if (lane == 0) prefix[s + 1] = u * a.n_kv;
@@ -257,7 +262,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
   }
   __syncthreads();
   const uint32_t total = prefix[a.S];
-  const uint32_t quota = (total + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);  // steps of a warp
+  uint32_t quota = (total + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);  // steps of a warp
+  if (p.fixed > 0) quota = (total / p.fixed + gridDim.x - 1) / gridDim.x * (p.fixed / kWarps);
   const uint32_t b_begin = min(total, blockIdx.x * kWarps * quota), b_end = min(total, b_begin + kWarps * quota);
   const uint32_t u_begin = min(total, b_begin + warp * quota), u_end = min(total, u_begin + quota);
   if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
     cur.at = u_begin;
     cur.item0 = prefix[lo];
     for (cur.rt = 0;; ++cur.rt) {
-      cur.item_steps = steps_of<kTile>(tile_keys(cur.seq, cur.rt, kRows, group));
+      cur.item_steps = item_steps_of(tile_keys(cur.seq, cur.rt, kRows, group));
       const uint32_t next = cur.item0 + static_cast<uint32_t>(cur.item_steps) * a.n_kv;
       if (next > cur.at) break;
       cur.item0 = next;
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
             q.seq = load_seq(a, ++q.s);
           } while (q.seq.n_new == 0 && q.s + 1 < a.S);
         }
-        q.item_steps = steps_of<kTile>(tile_keys(q.seq, q.rt, kRows, group));
+        q.item_steps = item_steps_of(tile_keys(q.seq, q.rt, kRows, group));
       }
     }
     return true;
@@ -779,6 +785,16 @@ cudaError_t launch(AttnParams p, const CUtensorMap& tmK, const CUtensorMap& tmV,
   p.desc = static_cast<int4*>(workspace);
   p.slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16 * static_cast<size_t>(blocks));
   p.warp_slots = p.slots + static_cast<size_t>(blocks) * 2 * Cfg::kSlotFloats;
+  // Where no sequence can have many steps, items are padded to a block's warps, so that none is shared between
+  // blocks and the second kernel need not be launched.  The padding costs balance: with up to 8 steps a
+  // sequence always (a warp then takes one or two steps, or whole items where there are many), with up to 8
+  // steps a warp only where every item has a block of its own.
+  const int64_t most = (static_cast<int64_t>(p.a.max_pages) * p.a.page + Cfg::kTile - 1) / Cfg::kTile;
+  const int64_t rows = static_cast<int64_t>(p.a.max_new) * (p.a.n_heads / p.a.n_kv);
+  const int64_t items = p.a.S * ((rows + Cfg::kRows - 1) / Cfg::kRows) * p.a.n_kv;
+  p.fixed = most <= kFixedMax || (most <= kFixedMax * Cfg::kWarps && items <= blocks)
+                ? static_cast<int>((most + Cfg::kWarps - 1) / Cfg::kWarps * Cfg::kWarps)
+                : 0;
   auto kern = attn_kv8_kernel<D, NT>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), 227 * 1024, allowed);
@@ -788,8 +804,7 @@ cudaError_t launch(AttnParams p, const CUtensorMap& tmK, const CUtensorMap& tmV,
     kern<<<blocks, Cfg::kThreads, smem, stream>>>(tmK, tmV, p);
   }
   e = cudaGetLastError();
-  // no item is longer than a block's run when a sequence cannot pass one step: nothing to join
-  if (e != cudaSuccess || static_cast<int64_t>(p.a.max_pages) * p.a.page <= Cfg::kTile) return e;
+  if (e != cudaSuccess || p.fixed > 0) return e;  // no item is shared
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the kernel before it

@@ -94,6 +94,29 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
   }
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // place of 16-byte chunk c (of 16: 8 dimensions each) of row r in a swizzled tile of two boxes
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return static_cast<uint32_t>((c >> 3) * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -258,15 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
           for (int i = 0; i < 16; ++i) x[o + i] = tb + 16 * g + i < end ? fmaf(x[o + i], f, fe) : -INFINITY;
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[o + i] = fmaf(x[o + i], f, fe);
+          for (int i = 0; i < 16; i += 2) {
+            const float2 v = fma2(make_float2(x[o + i], x[o + i + 1]), make_float2(f, f), make_float2(fe, fe));
+            x[o + i] = v.x;
+            x[o + i + 1] = v.y;
+          }
         }
-        float t0 = x[o], t1 = x[o + 1];
 #pragma unroll
-        for (int i = 2; i < 16; i += 2) {
-          t0 = fmaxf(t0, x[o + i]);
-          t1 = fmaxf(t1, x[o + i + 1]);
-        }
-        top = fmaxf(top, fmaxf(t0, t1));
+        for (int i = 0; i < 16; i += 2) top = max3(top, x[o + i], x[o + i + 1]);
       }
       exps = exps_next;
       // the row's maximum over all parts
@@ -301,15 +323,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       uint32_t pk[kCols / 2];
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        float s0 = 0.0f, s1 = 0.0f;
+        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float p0 = at_ex2(x[16 * g + 2 * i] - ref), p1 = at_ex2(x[16 * g + 2 * i + 1] - ref);
-          s0 += p0;
-          s1 += p1;
-          pk[8 * g + i] = pack_f16x2(p0, p1);
+          const float2 d = add2(make_float2(x[16 * g + 2 * i], x[16 * g + 2 * i + 1]), make_float2(-ref, -ref));
+          const float2 e = make_float2(at_ex2(d.x), at_ex2(d.y));
+          sum = add2(sum, e);
+          pk[8 * g + i] = pack_f16x2(e.x, e.y);
         }
-        l = fmaf(s0 + s1, back[g], l);
+        l = fmaf(sum.x + sum.y, back[g], l);
       }
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->p_empty[b], par ^ 1u, abort_flag));
       if (!ok) break;
