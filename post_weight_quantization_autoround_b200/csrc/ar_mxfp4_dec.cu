@@ -381,12 +381,23 @@ cudaError_t launch_mxfp4_dec(const uint16_t* A, int T, const uint8_t* codes, con
   p.spans = (K + kSpan - 1) / kSpan;
   p.tiles = (N + kRows - 1) / kRows;
   p.wide = K % kSpan == 0;
-  // CTAs that share k: two (one span: one); four where two would not hold the activations, or where
-  // there are too few row tiles for two to fill the GPU
-  int cl = p.spans < 2 ? 1 : 2;
+  // CTAs that share k.  A cluster's row tiles come in whole numbers, so more CTAs to a cluster balance better and
+  // each holds fewer of the activations; meeting in distributed shared memory costs about what 22 units do (2 of
+  // 45 us at 392 units).  8 tokens through 4096 x 4096: 12.0 us with two, 10.6 alone; one token is 10.5 either
+  // way, the host's time for a call.
   auto act = [&](int n) { const int s = (p.spans + n - 1) / n; return s * (T * 512 + 32); };
-  if (p.spans >= 4 && (act(2) > kActBytesMax || 2 * p.tiles < num_sms())) cl = 4;
-  if (act(cl) > kActBytesMax) return cudaErrorNotSupported;
+  int cl = 0;
+  int64_t best = INT64_MAX;
+  for (int n = 1; n <= 4 && n <= p.spans; n *= 2) {
+    if (act(n) > kActBytesMax) continue;
+    const int clusters = num_sms() / n;
+    const int64_t cost = static_cast<int64_t>((p.tiles + clusters - 1) / clusters) * ((p.spans + n - 1) / n) + (n > 1 ? 22 : 0);
+    if (cost < best) {
+      best = cost;
+      cl = n;
+    }
+  }
+  if (cl == 0) return cudaErrorNotSupported;
   p.spans_cta = (p.spans + cl - 1) / cl;
   p.stages = (kSmemMax - kFixedBytes - act(cl)) / kRingBytes;
   if (p.stages > kStagesMax) p.stages = kStagesMax;
