@@ -530,10 +530,10 @@ AR_API ar_status ar_tune_step_mxfp4(const uint16_t* W, float* V, float* alpha, i
  *           weights, 255 makes the whole row NaN
  *   out     bf16 [T][N] (round to nearest even of fp32 sums), 16-byte aligned
  * Weights are exact in bf16, so only the fp32 accumulation and the output round.
- * Small T decodes against the packed weights; larger T runs a tcgen05 GEMM that
- * dequantizes on the way; at T >= 512 with N % 8 == 0 and a workspace the weights are
- * expanded once into it and the pair GEMM runs (without a workspace: the
- * dequantizing GEMM).  Results are deterministic for given sizes.
+ * T <= 8 decodes against the packed weights (mma.sync); larger T runs a tcgen05 GEMM
+ * that expands them on the way, 256 tokens a tile; at T >= 2048 with N % 8 == 0, K <= 8192
+ * and a workspace the weights are expanded once into it and the pair GEMM runs (without
+ * a workspace: the GEMM that expands on the way).  Results are deterministic for given sizes.
  * Needs 1 <= T < 2^31, N >= 1, K % 32 == 0.
  * workspace: ar_mxfp4_gemm_workspace bytes (device, 256-byte aligned), or NULL. */
 AR_API size_t ar_mxfp4_gemm_workspace(int64_t T, int64_t N, int64_t K);

@@ -1186,11 +1186,11 @@ ar_status ar_tune_step_mxfp4(const uint16_t* W, float* V, float* alpha, int64_t 
   return end_call();
 }
 
-// From this many tokens the product expands the weights to bf16 once (the caller's workspace) and runs
-// the pair GEMM: the dequantizing GEMM would expand them again for every 128 tokens.
-static constexpr int64_t kMxExpandTokens = 512;
-
-static bool mxfp4_expands(int64_t T, int64_t N) { return T >= kMxExpandTokens && N % 8 == 0; }
+// Where the product expands the weights to bf16 once (the caller's workspace) and runs the pair GEMM, which
+// overlaps its tiles' ends with the next tiles; the GEMM that expands on the way does not, and a short K has
+// many ends.  Measured (us, expanding first / on the way): 11008 x 4096 at 1024 tokens 134 / 121, at 2048
+// 186 / 197, at 4096 327 / 372; 8192 x 28672 at 2048 808 / 747, at 4096 1436 / 1394.
+static bool mxfp4_expands(int64_t T, int64_t N, int64_t K) { return T >= 2048 && N % 8 == 0 && K <= 8192; }
 
 size_t ar_mxfp4_gemm_workspace(int64_t T, int64_t N, int64_t K) {
   begin_call();
@@ -1199,7 +1199,7 @@ size_t ar_mxfp4_gemm_workspace(int64_t T, int64_t N, int64_t K) {
     fail(AR_ERR_INVALID_ARG, "T, N, K must be in 1..2^31-1");
     return 0;
   }
-  return mxfp4_expands(T, N) ? align_up(static_cast<size_t>(N * K) * 2, 256) : 256;
+  return mxfp4_expands(T, N, K) ? align_up(static_cast<size_t>(N * K) * 2, 256) : 256;
 }
 
 ar_status ar_mxfp4_gemm(const uint16_t* A, int64_t T, const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t K,
@@ -1217,7 +1217,7 @@ ar_status ar_mxfp4_gemm(const uint16_t* A, int64_t T, const uint8_t* codes, cons
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int Ti = static_cast<int>(T), Ni = static_cast<int>(N), Ki = static_cast<int>(K);
   cudaError_t e;
-  if (workspace && mxfp4_expands(T, N)) {
+  if (workspace && mxfp4_expands(T, N, K)) {
     const size_t need = static_cast<size_t>(N * K) * 2;
     if (workspace_bytes < need) return fail(AR_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(AR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -1238,7 +1238,7 @@ static ar_status kv8_args(const ar_kv8_cfg* cfg, int64_t T, const int32_t* cu_se
   if (!cfg) return fail(AR_ERR_INVALID_ARG, "cfg is NULL");
   if (cfg->n_heads <= 0 || cfg->n_kv_heads <= 0 || cfg->n_heads % cfg->n_kv_heads != 0)
     return fail(AR_ERR_INVALID_ARG, "n_heads must be a positive multiple of n_kv_heads");
-  if (cfg->n_heads > 65536) return fail(AR_ERR_UNSUPPORTED, "n_heads exceeds 65536");
+  if (cfg->n_heads > 65535) return fail(AR_ERR_UNSUPPORTED, "n_heads exceeds 65535");
   if (cfg->head_dim != 64 && cfg->head_dim != 128) return fail(AR_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
   if (cfg->page_size != 16 && cfg->page_size != 32 && cfg->page_size != 64 && cfg->page_size != 128)
     return fail(AR_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
@@ -1248,7 +1248,7 @@ static ar_status kv8_args(const ar_kv8_cfg* cfg, int64_t T, const int32_t* cu_se
   if (cfg->max_pages > (1 << 30) / cfg->page_size) return fail(AR_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^30");
   if (T < 1 || S < 1 || max_new < 1) return fail(AR_ERR_INVALID_ARG, "T, S, max_new must be positive");
   if (S > kKv8MaxSeqs) return fail(AR_ERR_UNSUPPORTED, "more than %d sequences", kKv8MaxSeqs);
-  if (T > INT32_MAX / cfg->n_heads) return fail(AR_ERR_UNSUPPORTED, "T * n_heads exceeds 2^31-1");
+  if (T > (1 << 30) || T > INT32_MAX / cfg->n_heads) return fail(AR_ERR_UNSUPPORTED, "T exceeds 2^30 or T * n_heads 2^31-1");
   if (max_new > T) return fail(AR_ERR_INVALID_ARG, "max_new=%lld exceeds T=%lld", (long long)max_new, (long long)T);
   *a = Kv8Args{};
   a->cu = cu_seqlens;

@@ -378,14 +378,14 @@ cudaError_t launch_mxfp4_dec(const uint16_t* A, int T, const uint8_t* codes, con
   p.T = T;
   p.N = N;
   p.K = K;
-  p.spans = (K + kSpan - 1) / kSpan;
-  p.tiles = (N + kRows - 1) / kRows;
+  p.spans = static_cast<int>((static_cast<int64_t>(K) + kSpan - 1) / kSpan);
+  p.tiles = static_cast<int>((static_cast<int64_t>(N) + kRows - 1) / kRows);
   p.wide = K % kSpan == 0;
   // CTAs that share k.  A cluster's row tiles come in whole numbers, so more CTAs to a cluster balance better and
   // each holds fewer of the activations; meeting in distributed shared memory costs about what 22 units do (2 of
   // 45 us at 392 units).  8 tokens through 4096 x 4096: 12.0 us with two, 10.6 alone; one token is 10.5 either
   // way, the host's time for a call.
-  auto act = [&](int n) { const int s = (p.spans + n - 1) / n; return s * (T * 512 + 32); };
+  auto act = [&](int n) { return static_cast<int64_t>((p.spans + n - 1) / n) * (T * 512 + 32); };
   int cl = 0;
   int64_t best = INT64_MAX;
   for (int n = 1; n <= 4 && n <= p.spans; n *= 2) {
@@ -399,9 +399,10 @@ cudaError_t launch_mxfp4_dec(const uint16_t* A, int T, const uint8_t* codes, con
   }
   if (cl == 0) return cudaErrorNotSupported;
   p.spans_cta = (p.spans + cl - 1) / cl;
-  p.stages = (kSmemMax - kFixedBytes - act(cl)) / kRingBytes;
+  const int act_bytes = static_cast<int>(act(cl));
+  p.stages = (kSmemMax - kFixedBytes - act_bytes) / kRingBytes;
   if (p.stages > kStagesMax) p.stages = kStagesMax;
-  const int smem = kFixedBytes + p.stages * kRingBytes + act(cl);
+  const int smem = kFixedBytes + p.stages * kRingBytes + act_bytes;
   CUtensorMap tmW;
   cudaError_t e = make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, codes, static_cast<uint64_t>(N),
                                static_cast<uint64_t>(K) / 8, 32, kRows, CU_TENSOR_MAP_SWIZZLE_128B);

@@ -390,7 +390,8 @@ cudaError_t launch_tn(const uint16_t* A, const CUtensorMap& tmW, TcParams p, int
   cudaError_t e = make_tmap_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, static_cast<uint64_t>(p.T),
                                static_cast<uint64_t>(K), kStageK, TN, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((p.N + kRows - 1) / kRows) * (p.t_tiles = (p.T + TN - 1) / TN);
+  p.t_tiles = static_cast<int>((static_cast<int64_t>(p.T) + TN - 1) / TN);
+  const int64_t tiles = (static_cast<int64_t>(p.N) + kRows - 1) / kRows * p.t_tiles;
   if (tiles > INT32_MAX / 4) return cudaErrorInvalidValue;
   // CTAs that split K, while they would all be resident and each keeps two slots
   const int slots = (p.stages + kStagesPerSlot - 1) / kStagesPerSlot;
@@ -412,7 +413,7 @@ cudaError_t launch_mxfp4_tc(const uint16_t* A, int T, const uint8_t* codes, cons
   p.N = N;
   p.T = T;
   p.blocks = K / 32;
-  p.stages = (K + kStageK - 1) / kStageK;
+  p.stages = static_cast<int>((static_cast<int64_t>(K) + kStageK - 1) / kStageK);
   p.wide = K % 256 == 0;
   CUtensorMap tmW;
   cudaError_t e = make_tmap_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, codes, static_cast<uint64_t>(N),
