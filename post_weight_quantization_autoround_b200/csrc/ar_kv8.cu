@@ -159,8 +159,7 @@ __global__ void __launch_bounds__(THREADS, RING ? 512 / THREADS : 4)
   constexpr int kPass = THREADS / kLanes;    // tokens at once
   constexpr int kSlots = PASSES * kPass;     // tokens
   constexpr int kWarps = THREADS / 32;
-  constexpr int kHalfBytes = kSlots * D;     // a box: the tokens' half heads
-  constexpr int kUnitBytes = 2 * kHalfBytes;
+  constexpr int kUnitBytes = kSlots * D * 2;  // a box: a head of the page's tokens
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));  // TMA boxes
   __shared__ uint2 warp_max[2][kWarps];
@@ -225,8 +224,6 @@ __global__ void __launch_bounds__(THREADS, RING ? 512 / THREADS : 4)
     const int col = (j == 0 ? a.n_heads + h : j == 1 ? a.n_heads + a.n_kv + h : h * group + j - 2) * D;
     mbar_arrive_expect_tx(&ctl.full[slot_u], kUnitBytes);
     tma_load_2d(ring + slot_u * kUnitBytes, &tm, &ctl.full[slot_u], col, static_cast<int>(first_row) + (lo - start));
-    tma_load_2d(ring + slot_u * kUnitBytes + kHalfBytes, &tm, &ctl.full[slot_u], col + kHalf,
-                static_cast<int>(first_row) + (lo - start));
     ++issued;
   };
   if (RING) {
@@ -251,8 +248,8 @@ __global__ void __launch_bounds__(THREADS, RING ? 512 / THREADS : 4)
     if (tid == 0 && alive && issued < units && issued - kRing < u) issue();
   };
   auto unit = [&](int u, int p) {
-    const uint4* at = reinterpret_cast<const uint4*>(ring + (u % kRing) * kUnitBytes + (slot + p * kPass) * (kHalf * 2) + el * 2);
-    return Raw{at[0], at[kHalfBytes / 16]};
+    const uint4* at = reinterpret_cast<const uint4*>(ring + (u % kRing) * kUnitBytes + (slot + p * kPass) * (D * 2) + el * 2);
+    return Raw{at[0], at[kHalf / 8]};
   };
   const bool older = lo > page0;
   int buf = 0;
@@ -402,9 +399,9 @@ cudaError_t append(const Kv8Args& a, const uint16_t* qkv, const RopeTurns& turns
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed);
   if (e != cudaSuccess) return e;
   if (RING) {
-    // boxes of half a head: D / 2 columns of the page's tokens
+    // a box: one head's columns of the page's tokens
     e = make_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, qkv, static_cast<uint64_t>(a.T),
-                     static_cast<uint64_t>(a.n_heads + 2 * a.n_kv) * D, D / 2, kSlots, CU_TENSOR_MAP_SWIZZLE_NONE);
+                     static_cast<uint64_t>(a.n_heads + 2 * a.n_kv) * D, D, kSlots, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
   }
   {
