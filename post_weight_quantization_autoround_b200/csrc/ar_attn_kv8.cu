@@ -30,6 +30,10 @@
 //    joined from unnormalised sums in the workspace, by its block at the end of the
 //    block's run, and by a second kernel where several blocks share it; always in the
 //    order of the tokens: no atomics, the same result every time.
+//
+// 64 sequences up to 8191 keys, 64 heads over 8 of 128 (572 MB): 115 us for this kernel, 119 with the second,
+// 4.8 TB/s, 75 % of a copy's rate; 2 x 131000 keys 104 us, 5.2 TB/s.  While an SM is busy it takes its share of the
+// full rate, but equal runs end 134 to 170 thousand cycles in: some SMs are served faster than others.
 #include "ar_internal.h"
 
 namespace ar {

@@ -17,7 +17,10 @@
 //    swizzle; the same layout serves K as the K-major and V as the MN-major operand).
 //
 // A block of 128 x 128 costs 1024 cycles of MMAs and the same of exponentials (16 a cycle and SM):
-// the two overlap, so half the tensor rate is what exponentials leave.
+// the two overlap, so half the tensor rate is what exponentials leave.  2 x 512 new tokens of 4000, 64 heads
+// over 8: 199 us, 412 TFLOP/s, tensor pipe 20 %; a block takes 3900 cycles, because the softmax warps of a block
+// wait for one another's maxima and so reach their exponentials together.  Eight softmax warps 258 us; the
+// mma.sync kernel 587 us.
 // TMEM columns: S buffers [0, 256), P buffers [256, 384), O [384, 512).
 #include "ar_attn_tc.cuh"
 

@@ -25,8 +25,8 @@
 //  * Up to 128 threads' worth of new tokens in a page (a decode step): loads straight to
 //    registers, idle threads take query heads.
 //  * More: a head's tokens come as TMA boxes through a ring in shared memory, so
-//    that loads stay in flight across the barrier; holding them in registers ran at half
-//    the rate (8 prompts of 2048 tokens, 32 + 32 heads of 128: 210 us).
+//    that loads stay in flight across the barrier: 8 prompts of 2048 tokens, 32 + 32 heads of 128, 162 us
+//    (671 MB, 4.1 TB/s, 63 % of a copy's rate; 74 M instructions at 1.7 a cycle); in registers 210 us.
 #include <cuda_fp8.h>
 
 #include "ar_internal.h"
@@ -431,8 +431,11 @@ cudaError_t launch_kv8_append(const Kv8Args& a, const uint16_t* qkv, double rope
                               uint8_t* v_pages, uint8_t* k_scales, uint8_t* v_scales, uint16_t* q_out,
                               cudaStream_t stream) {
   RopeTurns t{};
-  for (int i = 0; i < a.head_dim / 2; ++i)
-    t.f[i] = pow(rope_base, -2.0 * i / a.head_dim) * 0.15915494309189533577;  // 1 / (2 pi)
+  // one power, then products: 64 roundings of 2^-53 turn position 10^9 by 10^-5 rad at most, and 64 powers would be a
+  // fifth of a small call's time on the host
+  const double step = pow(rope_base, -2.0 / a.head_dim);
+  t.f[0] = 0.15915494309189533577;  // 1 / (2 pi)
+  for (int i = 1; i < a.head_dim / 2; ++i) t.f[i] = t.f[i - 1] * step;
   if (a.head_dim == 128) return append_d<128>(a, qkv, t, k_pages, v_pages, k_scales, v_scales, q_out, stream);
   return append_d<64>(a, qkv, t, k_pages, v_pages, k_scales, v_scales, q_out, stream);
 }

@@ -17,6 +17,11 @@
 //    part in a slot of its own.  The CTAs of a cluster split k, so that a block's share of
 //    the activations stays in shared memory; their sums meet through distributed shared
 //    memory.  Parts are added in a fixed order.
+//
+// 5 tokens through 8192 x 28672 (125 MB of codes and scales): 45 us, 2.8 TB/s, 43 % of a copy's
+// rate; 58 % of the issue slots and 54 % of the integer pipe are busy, about 56 instructions a
+// block and tile, half of them the box's control.  One token 39 us (34 of them the same loop).
+// Four CTAs to a cluster instead of two 48 us (132 of 148 SMs hold clusters of four), 8 warps 66 us.
 #include "ar_internal.h"
 
 namespace ar {
