@@ -461,3 +461,120 @@ def test_a_decode_step_of_the_operators_together(ar):
     assert (whole[-1] - steps[-1]).norm() <= 2.0 ** -5 * whole[-1].norm()
     for a, b in zip(ca[2:], cb[2:]):
         assert torch.equal(a, b)  # the scales end where the whole prompt put them
+
+
+@pytest.mark.parametrize("n_heads,n_new", [(4, 1), (64, 300)])
+def test_pool_past_32_bits(ar, n_heads, n_new):
+    """A pool of more than 2^32 bytes whose last pages hold the sequence: the same codes and outputs as from a small pool,
+    for the decode kernel and for the prompts' one."""
+    n_kv, d, page, length = 2, 128, 128, 700
+    pages = -(-length // page)
+    rng = np.random.default_rng(n_heads)
+    cu, cud, ld = _index([n_new], [length])
+    qkv = torch.from_numpy(rng.normal(size=(n_new, (n_heads + 2 * n_kv) * d)).astype(np.float32)).bfloat16().cuda()
+    small = Cache([length], n_heads, n_kv, d, page, 3, garbage=False).gpu()
+    big = 140_000
+    table = np.arange(pages, dtype=np.int32)[None]
+    results = []
+    for total in (small[0].shape[0], big):
+        base = 0 if total != big else big - pages
+        if total == big:
+            pool = [torch.empty((total, *x.shape[1:]), dtype=torch.uint8, device="cuda") for x in small]
+            for x, y in zip(pool, small):
+                x[base:] = y[:pages]
+            assert pool[0].numel() > 2 ** 32
+        else:
+            pool = [x.clone() for x in small]
+        t = torch.from_numpy(table + base).cuda()
+        q, out = (torch.empty(n_new, n_heads * d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        ar.ar_kv8_append(qkv, cud, ld, t, *pool, q, n_new)
+        ws = torch.empty(ar.ar_attention_kv8_workspace(n_new, 1, n_new, n_heads, n_kv, d, page, total, pages), dtype=torch.uint8, device="cuda")
+        ar.ar_attention_kv8(q, cud, ld, t, *pool, out, n_new, ws)
+        assert ("attn_kv8_tc_kernel" in ar.ar_last_kernels()) == (n_new > 1) and ar.ar_get_device_status() == ar.AR_OK
+        results.append([x[base:base + pages].clone() for x in pool] + [q, out])
+        del pool
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_decode_loop_in_a_graph(ar):
+    """One captured append and attention, replayed for every token while the lengths grow, against calls made one by one;
+    the graph runs on a stream of its own."""
+    n_heads, n_kv, d, page, start, steps = 8, 2, 128, 16, 13, 40
+    pages = -(-(start + steps) // page) + 1
+    rng = np.random.default_rng(0)
+    c = Cache([start, 2 * page], n_heads, n_kv, d, page, 7, max_pages=pages + 2)
+    total = c.k.shape[0] + 2 * pages
+    gpu = [torch.cat([x, torch.zeros(2 * pages, *x.shape[1:], dtype=x.dtype, device="cuda")]) for x in c.gpu()]
+    table = c.table.copy()
+    nxt = c.k.shape[0]
+    for s in range(2):
+        for i in range(table.shape[1]):
+            if table[s, i] < 0:
+                table[s, i] = nxt
+                nxt = nxt + 1 if nxt + 1 < total else nxt
+    table = torch.from_numpy(table).cuda()
+    tokens = [torch.from_numpy(rng.normal(size=(2, (n_heads + 2 * n_kv) * d)).astype(np.float32)).bfloat16().cuda() for _ in range(steps)]
+    cu, cud, _ = _index([1, 1], [start, 2 * page])
+
+    def buffers():
+        return dict(pool=[x.clone() for x in gpu], lens=torch.tensor([start, 2 * page], dtype=torch.int32, device="cuda"),
+                    q=torch.empty(2, n_heads * d, dtype=torch.bfloat16, device="cuda"),
+                    out=torch.empty(2, n_heads * d, dtype=torch.bfloat16, device="cuda"), qkv=torch.empty_like(tokens[0]),
+                    ws=torch.empty(ar.ar_attention_kv8_workspace(2, 2, 1, n_heads, n_kv, d, page, total, table.shape[1]), dtype=torch.uint8, device="cuda"))
+
+    def step(b):
+        b["lens"] += 1
+        ar.ar_kv8_append(b["qkv"], cud, b["lens"], table, *b["pool"], b["q"], 1)
+        ar.ar_attention_kv8(b["q"], cud, b["lens"], table, *b["pool"], b["out"], 1, b["ws"])
+
+    one, two = buffers(), buffers()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(two)
+    st = torch.cuda.Stream()
+    for x in tokens:
+        one["qkv"].copy_(x)
+        two["qkv"].copy_(x)
+        step(one)
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            g.replay()
+        torch.cuda.current_stream().wait_stream(st)
+        assert torch.equal(one["out"], two["out"])
+    assert ar.ar_get_device_status() == ar.AR_OK and one["lens"].tolist() == [start + steps, 2 * page + steps]
+    for a, b in zip(one["pool"], two["pool"]):
+        assert torch.equal(a, b)
+
+
+def test_binding_refusals(ar):
+    c = Cache([20], 4, 2, 64, 16, 1)
+    cu, cud, ld = _index([1], [20])
+    k, v, ks, vs = c.gpu()
+    t = torch.from_numpy(c.table).cuda()
+    q = torch.zeros(1, 256, dtype=torch.bfloat16, device="cuda")
+    ws = _workspace(ar, c, 1, 1)
+    good = dict(q=q, cu_seqlens=cud, seq_lens=ld, page_table=t, k_pages=k, v_pages=v, k_scales=ks, v_scales=vs, out=torch.empty_like(q), max_new=1, workspace=ws)
+    ar.ar_attention_kv8(**good)
+    wide = torch.zeros(1, 512, dtype=torch.bfloat16, device="cuda")
+    for name, bad in (("q", q.float()), ("out", wide), ("out", wide[:, ::2]), ("cu_seqlens", cud.long()), ("seq_lens", ld.cpu()),
+                      ("v_pages", v[:-1]), ("k_scales", ks.int()), ("page_table", t.cpu()), ("seq_lens", ld.repeat(2)), ("workspace", ws[:16])):
+        with pytest.raises(ar.ARError):
+            ar.ar_attention_kv8(**{**good, name: bad})
+    qkv = torch.zeros(1, 8 * 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ar.ARError):
+        ar.ar_kv8_append(qkv, cud, ld, t, k, v, ks, vs, q[:, ::2], 1)
+    with pytest.raises(ar.ARError):
+        ar.ar_kv8_append(qkv[:, :500], cud, ld, t, k, v, ks, vs, q, 1)
+    W = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    for args in ((W.float(), None, None, W), (W, W, None, W), (W, None, None, W.t()), (W, None, W.float(), W), (W.cpu(), None, None, W)):
+        with pytest.raises(ar.ARError):
+            ar.ar_qdq_mxfp4(*args)
+    codes, scales = torch.zeros(8, 32, dtype=torch.uint8, device="cuda"), torch.zeros(8, 2, dtype=torch.uint8, device="cuda")
+    A = torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda")
+    for out in (torch.empty(3, 8, device="cuda"), torch.empty(8, 3, dtype=torch.bfloat16, device="cuda")):
+        with pytest.raises(ar.ARError):
+            ar.ar_mxfp4_gemm(A, codes, scales, out)
+    with pytest.raises(ar.ARError):
+        ar.ar_mxfp4_gemm(A, codes[:, :16], scales, torch.empty(3, 8, dtype=torch.bfloat16, device="cuda"))
+    assert ar.ar_get_device_status() == ar.AR_OK
