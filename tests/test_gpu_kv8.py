@@ -193,6 +193,35 @@ def test_attention_prompts_growing_scores_and_scales(ar):
     assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG and (out == 7.0).all()
 
 
+@pytest.mark.parametrize("page", [16, 128])
+def test_attention_prompts_of_one_tile(ar, page):
+    """Up to 128 rows a sequence and head: one tile, whose blocks two groups share by turns; lengths around whole blocks,
+    odd and even counts of them, maxima that grow, rows that see no key; a query that is not finite stays in its row."""
+    lens = [16, 17, 128, 129, 255, 256, 257, 384, 385, 1000, 5, 1300, 513]
+    news = [16, 15, 16, 1, 16, 7, 16, 16, 9, 16, 16, 16, 0]
+    c = Cache(lens, 96, 12, 128, page, page)
+    for s, n in enumerate(lens):
+        for i in range(-(-n // page)):
+            c.ks[c.table[s, i]] = 114 + min(13, i * page // 60 + s % 2)
+    cu, cud, ld = _index(news, lens)
+    T = cu[-1] + 2
+    q = torch.from_numpy(c.rng.normal(size=(T, 96 * 128)).astype(np.float32)).bfloat16().cuda()
+    lse = torch.full((T, 96), 3.0, device="cuda")
+    gpu = c.gpu()
+    out = _attend(ar, c, q, cud, ld, 16, gpu, lse=lse)
+    assert "attn_kv8_tc_kernel" in ar.ar_last_kernels() and ar.ar_get_device_status() == ar.AR_OK
+    _check(c, q, cu, out, lse)
+    assert (out[cu[-1]:] == 7.0).all() and (lse[cu[-1]:] == 3.0).all()
+    rows = [(cu[9] + 3, 40, "nan"), (cu[11], 0, "inf"), (cu[4] + 15, 95, "-inf")]
+    for t, h, x in rows:
+        q[t, h * 128 + 5] = float(x)
+    got = _attend(ar, c, q, cud, ld, 16, gpu)
+    for t, h, x in rows:
+        assert not torch.equal(got[t, h * 128:(h + 1) * 128], out[t, h * 128:(h + 1) * 128])
+        got[t, h * 128:(h + 1) * 128] = out[t, h * 128:(h + 1) * 128]
+    assert torch.equal(got, out)
+
+
 @pytest.mark.parametrize("n_heads,n_kv,d", [(8, 8, 128), (64, 4, 64), (24, 1, 128)])
 def test_attention_many_short_sequences(ar, n_heads, n_kv, d):
     """Many items to a block, most of them too short to give every warp a step, some in two pieces."""
