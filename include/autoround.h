@@ -595,7 +595,8 @@ AR_API ar_status ar_kv8_append(const ar_kv8_cfg* cfg, const uint16_t* qkv, int64
  * sm_scale 0 means 1/sqrt(head_dim).  A row that sees no key (a sequence shorter
  * than its new tokens) gets out 0 and lse -inf.  max_new: an upper bound of a
  * sequence's new tokens (longer ones are refused on the device).  It and T choose the
- * kernel: at head_dim 128, rows enough to fill tiles of 128 run on tcgen05, else
+ * kernel: at head_dim 128, rows enough to fill tiles of 128 run on tcgen05 (sequences
+ * of single tokens next to them on the other kernel, in the same call), else
  * mma.sync with every warp an equal share of all keys.
  * The result does not depend on timing; the lengths may change between replays
  * of a captured call.  Codes 0x7F and 0xFF (NaN) are not written by ar_kv8_append;

@@ -100,6 +100,7 @@ __device__ __forceinline__ Seq load_seq(const Kv8Args& a, int s) {
   if (!ok) raise_status(kStatusBadIndex);
   q.first = ok ? static_cast<int>(c0) : 0;
   q.n_new = ok ? static_cast<int>(rows) : 0;
+  if (a.split_rows > 0 && static_cast<int64_t>(q.n_new) * (a.n_heads / a.n_kv) >= a.split_rows) q.n_new = 0;  // the other kernel's
   q.len = ok ? static_cast<int>(len) : 0;
   return q;
 }
@@ -774,10 +775,20 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const AttnParams p) 
   }
 }
 
-// rows of a tile: the fewest of 8, 16, 32 that hold the longest sequence's rows
+// rows of a tile, in eights: the fewest of 8, 16, 32 that hold the longest sequence's rows
+int tiles_for(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 int tiles_of(const Kv8Args& a) {
-  const int64_t rows = static_cast<int64_t>(a.max_new) * (a.n_heads / a.n_kv);
-  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  return tiles_for(a.split_rows > 0 ? a.split_rows - 1 : static_cast<int64_t>(a.max_new) * (a.n_heads / a.n_kv));
+}
+
+// Where sequences of different numbers of new tokens may share a call that goes to tcgen05 (prompts next to single
+// tokens), those with no more rows than the smallest tile here that holds one token run here, where a long cache
+// is split over the GPU; a tile of the other kernel stays with one SM.  512 new tokens of 4000 next to 31 single ones of
+// 32000, 64 heads over 8: 455 us, all on tcgen05 1334; three prompts, where nothing is left for this kernel, 77 and 70.
+int split_rows_of(const Kv8Args& a) {
+  const int group = a.n_heads / a.n_kv;
+  if (a.T == static_cast<int64_t>(a.S) * a.max_new || group > 32 || !attn_kv8_tc_fits(a)) return 0;
+  return 8 * tiles_for(group) + 1;
 }
 
 template <int D, int NT>
@@ -837,7 +848,9 @@ double attn_kv8_steps(const Kv8Args& a) {
   return tiles * a.n_kv * (static_cast<double>(a.max_pages) * a.page / (nt == 4 ? kBox : 2 * kBox) + 1.0);
 }
 
-size_t attn_kv8_workspace(const Kv8Args& a) {
+size_t attn_kv8_workspace(const Kv8Args& args) {
+  Kv8Args a = args;
+  a.split_rows = split_rows_of(a);
   const int nt = tiles_of(a);
   if (a.head_dim == 128) return nt == 1 ? workspace_of<128, 1>() : nt == 2 ? workspace_of<128, 2>() : workspace_of<128, 4>();
   return nt == 1 ? workspace_of<64, 1>() : nt == 2 ? workspace_of<64, 2>() : workspace_of<64, 4>();
@@ -846,10 +859,13 @@ size_t attn_kv8_workspace(const Kv8Args& a) {
 cudaError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, float sm_scale, const uint8_t* k_pages,
                             const uint8_t* v_pages, const uint8_t* k_scales, const uint8_t* v_scales, uint16_t* out,
                             float* lse, void* workspace, cudaStream_t stream) {
-  if (attn_kv8_tc_fits(a))
-    return launch_attn_kv8_tc(a, q, sm_scale, k_pages, v_pages, k_scales, v_scales, out, lse, stream);
   AttnParams p{};
   p.a = a;
+  if (attn_kv8_tc_fits(a)) {
+    p.a.split_rows = split_rows_of(a);
+    const cudaError_t e = launch_attn_kv8_tc(p.a, q, sm_scale, k_pages, v_pages, k_scales, v_scales, out, lse, stream);
+    if (e != cudaSuccess || p.a.split_rows == 0) return e;
+  }
   p.q = q;
   p.ks = k_scales;
   p.vs = v_scales;
@@ -862,7 +878,7 @@ cudaError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, float sm_scale,
   cudaError_t e = make_tmap_2d(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, k_pages, rows, a.head_dim, a.head_dim, kBox, sw);
   if (e == cudaSuccess) e = make_tmap_2d(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, v_pages, rows, a.head_dim, a.head_dim, kBox, sw);
   if (e != cudaSuccess) return e;
-  const int nt = tiles_of(a);
+  const int nt = tiles_of(p.a);
   if (a.head_dim == 128)
     return nt == 1   ? launch<128, 1>(p, tmK, tmV, workspace, stream)
            : nt == 2 ? launch<128, 2>(p, tmK, tmV, workspace, stream)

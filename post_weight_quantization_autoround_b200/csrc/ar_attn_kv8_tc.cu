@@ -27,6 +27,7 @@
 // goes through it.  One tile a CTA with sixteen softmax warps took 199 us, the mma.sync kernel 587 us; the
 // scores held in registers (168 a thread, MMAs issued by a softmax warp) 204 us, two threads a row 188 us.
 // TMEM columns: S and P of the groups [0, 256), O [256, 512).
+#include <algorithm>
 #include <type_traits>
 
 #include "ar_attn_tc.cuh"
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
   }
   const int n_new = static_cast<int>(new64), len = static_cast<int>(len64), first = static_cast<int>(c0);
   const int n_rows = n_new * group;
+  if (n_rows < a.split_rows) return;
   const int tiles = (n_rows + kCtaRows - 1) / kCtaRows;
   if (static_cast<int>(blockIdx.x) >= tiles) return;
   const int row0 = (tiles - 1 - static_cast<int>(blockIdx.x)) * kCtaRows;  // the longest rows first
@@ -600,11 +602,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
 // the keys over the GPU, 37 us and 1.65 us for every tile of 128 rows.  Both grow alike with the keys.
 // Measured, 64 heads over 8, one sequence of 4000: 64 new tokens 105 against 91 us, 100: 107 against 124, 256: 106
 // against 249; 16 sequences of 33 new tokens, 32 heads over 4: 106 against 271.
+// Where lengths differ, short sequences run on the other kernel beside this one; how many are not short is taken from
+// the tokens that are left when every sequence has one.
 bool attn_kv8_tc_fits(const Kv8Args& a) {
-  const int64_t group = a.n_heads / a.n_kv, rows = a.T * group;
+  const int64_t group = a.n_heads / a.n_kv;
   if (a.head_dim != kD || a.S > 65535 || a.n_kv > 65535 || a.max_new * group < kBlk) return false;
+  int64_t seqs = a.S;
+  if (group <= 32 && a.max_new > 1 && a.T > a.S) seqs = std::min<int64_t>(seqs, (a.T - a.S + a.max_new - 2) / (a.max_new - 1));
+  const int64_t rows = std::max<int64_t>(a.T - (a.S - seqs), 1) * group;
   const int64_t tiles = (rows + kBlk - 1) / kBlk * a.n_kv;
-  const int64_t ctas = (rows + kCtaRows - 1 + a.S * (kCtaRows / 2)) / kCtaRows * a.n_kv;
+  const int64_t ctas = (rows + kCtaRows - 1 + seqs * (kCtaRows / 2)) / kCtaRows * a.n_kv;
   const int64_t waves = (ctas + num_sms() - 1) / num_sms();
   return tiles + 22 >= 64 * waves;
 }

@@ -223,6 +223,7 @@ struct Kv8Args {
   const int32_t* table;  // [S][max_pages]
   int64_t T;             // rows of the new tokens' arrays
   int S, n_heads, n_kv, head_dim, page, max_pages, max_new;
+  int split_rows;  // attention: sequences of fewer rows a head run on mma.sync, the others on tcgen05; 0: one kernel runs all
   int64_t n_pages;
 };
 constexpr int kKv8MaxSeqs = 4096;

@@ -193,6 +193,27 @@ def test_attention_prompts_growing_scores_and_scales(ar):
     assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG and (out == 7.0).all()
 
 
+def test_attention_prompts_next_to_single_tokens(ar):
+    """Sequences of a few rows run on mma.sync, long and short, the others of the same call on tcgen05."""
+    news, lens = [200, 1, 1, 129, 1, 3, 0, 4, 1, 40], [900, 5000, 1, 129, 64, 700, 50, 300, 0, 9]
+    c = Cache(lens, 64, 8, 128, 32, 5)
+    cu, cud, ld = _index(news, lens)
+    T = cu[-1] + 2
+    q = torch.from_numpy(c.rng.normal(size=(T, 64 * 128)).astype(np.float32)).bfloat16().cuda()
+    lse = torch.full((T, 64), 3.0, device="cuda")
+    gpu = c.gpu()
+    out = _attend(ar, c, q, cud, ld, 200, gpu, lse=lse)
+    kernels = ar.ar_last_kernels().split(";")
+    assert "attn_kv8_tc_kernel" in kernels and "attn_kv8_kernel" in kernels and ar.ar_get_device_status() == ar.AR_OK
+    _check(c, q, cu, out, lse)
+    assert (out[cu[-1]:] == 7.0).all() and (lse[cu[-1]:] == 3.0).all()
+    assert torch.equal(out, _attend(ar, c, q, cud, ld, 200, gpu))
+    # a sequence that does not fit is left as it was by both kernels
+    cu[5] = cu[4] - 1
+    out2 = _attend(ar, c, q, torch.from_numpy(cu).cuda(), ld, 200, gpu)
+    assert ar.ar_get_device_status() == ar.AR_ERR_INVALID_ARG and torch.equal(out2[:cu[4] - 1], out[:cu[4] - 1])
+
+
 @pytest.mark.parametrize("page", [16, 128])
 def test_attention_prompts_of_one_tile(ar, page):
     """Up to 128 rows a sequence and head: one tile, whose blocks two groups share by turns; lengths around whole blocks,
