@@ -781,13 +781,13 @@ int tiles_of(const Kv8Args& a) {
   return tiles_for(a.split_rows > 0 ? a.split_rows - 1 : static_cast<int64_t>(a.max_new) * (a.n_heads / a.n_kv));
 }
 
-// Where sequences of different numbers of new tokens may share a call that goes to tcgen05 (prompts next to single
-// tokens), those with no more rows than the smallest tile here that holds one token run here, where a long cache
-// is split over the GPU; a tile of the other kernel stays with one SM.  512 new tokens of 4000 next to 31 single ones of
-// 32000, 64 heads over 8: 455 us, all on tcgen05 1334; three prompts, where nothing is left for this kernel, 77 and 70.
+// Where a call that goes to tcgen05 seems to have short sequences too (prompts next to single tokens), those with no
+// more rows than the smallest tile here that holds one token run here, where a long cache is split over the GPU; a
+// tile of the other kernel stays with one SM.  512 new tokens of 4000 next to 31 single ones of 32000, 64 heads
+// over 8: 453 us, all on tcgen05 1334; a launch with nothing left to do costs 6.
 int split_rows_of(const Kv8Args& a) {
   const int group = a.n_heads / a.n_kv;
-  if (a.T == static_cast<int64_t>(a.S) * a.max_new || group > 32 || !attn_kv8_tc_fits(a)) return 0;
+  if (attn_kv8_long_seqs(a) == a.S || !attn_kv8_tc_fits(a)) return 0;
   return 8 * tiles_for(group) + 1;
 }
 

@@ -597,18 +597,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
 
 }  // namespace
 
+// How many of a call's sequences bring more than a few rows, as far as the host can tell: by the tokens that are
+// left when every sequence has one.
+int64_t attn_kv8_long_seqs(const Kv8Args& a) {
+  if (a.n_heads / a.n_kv > 32 || a.max_new == 1 || a.T <= a.S) return a.S;
+  return std::min<int64_t>(a.S, (a.T - a.S + a.max_new - 2) / (a.max_new - 1));
+}
+
 // Whether a call runs faster on the kernel above.  It takes 106 us for a wave of CTAs (256 rows of one sequence
 // and head, or what is left of them: half a CTA a sequence on average) over 4000 keys; the other kernel, which splits
 // the keys over the GPU, 37 us and 1.65 us for every tile of 128 rows.  Both grow alike with the keys.
 // Measured, 64 heads over 8, one sequence of 4000: 64 new tokens 105 against 91 us, 100: 107 against 124, 256: 106
 // against 249; 16 sequences of 33 new tokens, 32 heads over 4: 106 against 271.
-// Where lengths differ, short sequences run on the other kernel beside this one; how many are not short is taken from
-// the tokens that are left when every sequence has one.
+// Short sequences next to long ones run on the other kernel beside this one.
 bool attn_kv8_tc_fits(const Kv8Args& a) {
   const int64_t group = a.n_heads / a.n_kv;
   if (a.head_dim != kD || a.S > 65535 || a.n_kv > 65535 || a.max_new * group < kBlk) return false;
-  int64_t seqs = a.S;
-  if (group <= 32 && a.max_new > 1 && a.T > a.S) seqs = std::min<int64_t>(seqs, (a.T - a.S + a.max_new - 2) / (a.max_new - 1));
+  const int64_t seqs = attn_kv8_long_seqs(a);
   const int64_t rows = std::max<int64_t>(a.T - (a.S - seqs), 1) * group;
   const int64_t tiles = (rows + kBlk - 1) / kBlk * a.n_kv;
   const int64_t ctas = (rows + kCtaRows - 1 + seqs * (kCtaRows / 2)) / kCtaRows * a.n_kv;

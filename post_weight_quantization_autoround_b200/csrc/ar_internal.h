@@ -240,6 +240,7 @@ cudaError_t launch_mxfp4_dec(const uint16_t* A, int T, const uint8_t* codes, con
                              uint16_t* out, cudaStream_t stream);
 // the same attention on tcgen05, head dimension 128 and many rows (ar_attn_kv8_tc.cu): whether it is the one to take
 bool attn_kv8_tc_fits(const Kv8Args& a);
+int64_t attn_kv8_long_seqs(const Kv8Args& a);
 cudaError_t launch_attn_kv8_tc(const Kv8Args& a, const uint16_t* q, float sm_scale, const uint8_t* k_pages,
                                const uint8_t* v_pages, const uint8_t* k_scales, const uint8_t* v_scales, uint16_t* out,
                                float* lse, cudaStream_t stream);
