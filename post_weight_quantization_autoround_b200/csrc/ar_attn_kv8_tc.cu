@@ -21,7 +21,7 @@
 // A tile's block of 128 keys costs 1024 cycles of MMAs and the same of exponentials (16 a cycle and SM).
 // The two groups take turns at the exponentials, so that one's MMAs run under the other's; left alone they
 // fall into step and both wait (184 us for the case below, 168 with the turns; 149 with two loads of S in
-// flight and a chunk kept for the second reading).  2 x 512 new tokens of 4000, 64 heads over 8: 144 us
+// flight and a chunk kept for the second reading).  2 x 512 new tokens of 4000, 64 heads over 8: 143 us
 // in a loop of calls, 570 TFLOP/s.  Of a group's 4800 cycles a block the scores take a quarter, the maximum an eighth,
 // the exponentials two fifths: shared memory, which the MMAs read at its full rate, slows all that
 // goes through it.  One tile a CTA with sixteen softmax warps took 199 us, the mma.sync kernel 587 us; the
