@@ -14,9 +14,12 @@
 //    register, with no scale applied.  Queries become f16 after a power-of-two
 //    normalisation per row (largest value in [2^13, 2^14)): what f16 loses is below 2^-38 of
 //    the row's largest value.  The scales are exponents and go into the softmax: with
-//    u = z log2(e) + e_v, P' = 2^(u - max u) carries the value scale and lies in [0, 1]
-//    whatever the scales, O = sum P' v', and the row sum adds P' 2^-e_v.  P' is f16 (2^-12
-//    relative, finer than the bf16 output), maximum, sum and O are fp32.
+//    u = z log2(e) + e_v, P' = 2^(u - max u + 15) carries the value scale and lies in [0, 2^15]
+//    whatever the scales, O = sum P' v', and the row sum adds P' 2^(-e_v - 15).  P' is f16 for the
+//    product: off by 2^-11 of itself at most (finer than the bf16 output) down to 2^-29 of the row's
+//    largest, and by 2^-40 of that below, which is why its range is used up to 2^15: behind a key
+//    that takes nearly all weight and has a small value, 10^5 keys still count.  The row sum takes the
+//    fp32 value; maximum, sum and O are fp32.
 //  * S^T leaves the tensor core with tokens along lanes' rows; movmatrix transposes the
 //    8 x 8 blocks into the B operand of O^T.  V^T comes from ldmatrix.trans on byte pairs:
 //    one byte permute separates even and odd dimensions.
@@ -42,6 +45,8 @@ namespace {
 constexpr int kBox = 16;       // tokens of a copy: a page is a multiple of it
 constexpr int kChunk = 32;     // steps whose pages and scales the lanes hold
 constexpr int kMaxWarps = 8;
+constexpr int kShift = 15;     // P' is at most 2^15
+constexpr float kUnshift = 1.0f / (1 << kShift);
 // Steps one after another that a warp may be given so that no item leaves its block (see the launch function).
 constexpr int kFixedMax = 8;
 
@@ -181,7 +186,7 @@ __device__ __forceinline__ void write_row(const AttnParams& p, const Seq& seq, i
   const int64_t row = static_cast<int64_t>(seq.first + tok) * p.a.n_heads + head * group + (rr - tok * group);
   const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
   *reinterpret_cast<uint2*>(p.out + row * D + d) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      make_uint2(pack_bf16x2(acc.x * kUnshift * inv, acc.y * kUnshift * inv), pack_bf16x2(acc.z * kUnshift * inv, acc.w * kUnshift * inv));
   if (p.lse && d == 0) p.lse[row] = sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
         const uint32_t ek = (exps >> (16 * h)) & 0xFFu, ev = (exps >> (16 * h + 8)) & 0xFFu;
         fk[h] = __uint_as_float(max(min(ek, 254u), 1u) << 23);
         fe[h] = static_cast<float>(static_cast<int>(ev) - 127);
-        back[h] = __uint_as_float(max(254u - min(ev, 253u), 1u) << 23);  // 2^-ev
+        back[h] = e8m0_inverse(ev, kShift);
       }
       const bool masked = tb + kTile > full_below || !whole_boxes;
       uint32_t pb[NT][kHalves][2];
@@ -552,7 +557,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
             o[mt][nt][3] *= sc[1];
           }
         }
-        const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
+        const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0] - kShift, m[nt][1] == -INFINITY ? 0.0f : m[nt][1] - kShift};
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
           float pr[4];
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
 #pragma unroll
             for (int mt = 0; mt < kMt; ++mt)
               *reinterpret_cast<uint32_t*>(p.out + row * D + 16 * mt + 2 * g) =
-                  pack_bf16x2(o[mt][nt][j] * inv, o[mt][nt][2 + j] * inv);
+                  pack_bf16x2(o[mt][nt][j] * kUnshift * inv, o[mt][nt][2 + j] * kUnshift * inv);
             if (p.lse && g == 0)
               p.lse[row] = l[nt][j] > 0.0f ? (m[nt][j] + log2f(l[nt][j])) * 0.6931471805599453f : -INFINITY;
           }

@@ -2,7 +2,7 @@
 // dimension 128, for calls with enough rows to fill tiles of 128 (prompts and pieces of prompts).
 // The method is attn_kv8_kernel's (ar_attn_kv8.cu): f16 operands, queries normalised
 // by a power of two per row, the caches' scales taken into the softmax's exponent,
-//   u = z log2(e) + e_v,  P' = 2^(u - m),  O = sum P' v',  l = sum P' 2^-e_v.
+//   u = z log2(e) + e_v,  P' = 2^(u - m + 11),  O = sum P' v',  l = sum P' 2^(-e_v - 11).
 //
 // One CTA per 256 rows (new token, head of the group) of one sequence and key/value head, over blocks of
 // 128 keys: two groups of warps with a tile of 128 rows each, which read the same expanded keys and values.
@@ -12,8 +12,11 @@
 //    O += P V in two halves of the keys (A = P as f16 pairs in tensor memory, B = V MN-major).
 //  * 2-9: softmax, a row a thread: warp w reads TMEM lanes 32 (w % 4) ...  S is read twice, for the row's
 //    maximum and for the exponentials, which go back over S as P from the last keys down, where S has been
-//    read.  The reference m only moves when a block's maximum passes it by 2^8, which f16 holds with
-//    room: O is then rescaled in tensor memory, which almost no block needs after the first.
+//    read.  The reference m only moves when a block's maximum passes it by 2^4: O is then rescaled in tensor
+//    memory, which few blocks need after the first.  P' reaches 2^15 there, and 2^11 at a reference that
+//    stays, so f16 is off by 2^-11 of a weight, or by 2^-36 of the row's largest where that is more (behind a
+//    key that takes nearly all weight and has a small value the others count all the same).  A wider margin
+//    leaves less below: 2^8 took 144 us where 2^4 takes 148 and 2^2 152 (the case below).
 //  * 10-13: expansion.  Codes come straight from the pages to registers a block ahead, each
 //    conversion instruction makes two f16, and the tile is written as the MMAs read it (128-byte
 //    swizzle; the same layout serves K as the K-major and V as the MN-major operand).
@@ -21,8 +24,8 @@
 // A tile's block of 128 keys costs 1024 cycles of MMAs and the same of exponentials (16 a cycle and SM).
 // The two groups take turns at the exponentials, so that one's MMAs run under the other's; left alone they
 // fall into step and both wait (184 us for the case below, 168 with the turns; 149 with two loads of S in
-// flight and a chunk kept for the second reading).  2 x 512 new tokens of 4000, 64 heads over 8: 143 us
-// in a loop of calls, 570 TFLOP/s.  Of a group's 4800 cycles a block the scores take a quarter, the maximum an eighth,
+// flight and a chunk kept for the second reading).  2 x 512 new tokens of 4000, 64 heads over 8: 148 us
+// in a loop of calls, 553 TFLOP/s.  Of a group's 4800 cycles a block the scores take a quarter, the maximum an eighth,
 // the exponentials two fifths: shared memory, which the MMAs read at its full rate, slows all that
 // goes through it.  One tile a CTA with sixteen softmax warps took 199 us, the mma.sync kernel 587 us; the
 // scores held in registers (168 a thread, MMAs issued by a softmax warp) 204 us, two threads a row 188 us.
@@ -49,7 +52,9 @@ constexpr int kThreads = (kExWarp0 + kExWarps) * 32;
 constexpr int kGroups = kBlk / 16;        // of 16 tokens: one scale each
 constexpr uint32_t kColS = 0, kColO = 2 * kBlk;  // of group g: + 128 g; P lies over the upper half of S
 constexpr uint32_t kColP = kColS + kBlk / 2;
-constexpr float kSlack = 8.0f;            // a block's maximum may pass the reference by 2^8
+constexpr int kSlack = 4;                 // a block's maximum may pass the reference by 2^4
+constexpr int kShift = 15 - kSlack;       // P' at the reference; the largest is 2^15
+constexpr float kUnshift = 1.0f / (1 << kShift);
 constexpr int kRowStep = kExThreads / 8;
 constexpr int kRowsPerThread = kBlk / kRowStep;  // 16-byte pieces of a tile a thread expands
 
@@ -343,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       Scales c;
       c.f = __uint_as_float(max(min(ek, 254u), 1u) << 23);
       c.fe = static_cast<float>(static_cast<int>(ev) - 127);
-      c.back = __uint_as_float(max(254u - min(ev, 253u), 1u) << 23);  // 2^-ev
+      c.back = e8m0_inverse(ev, kShift);
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->s_full[g], par, abort_flag))) return false;
       tc_fence_after();
       const int t0 = j * kBlk;
@@ -361,9 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       ld_wait(xb);
       top = chunk_max<kMask>(xa, c, fac, 2, t0 + 64, lim, bad, top);
       top = chunk_max<kMask>(xb, c, fac, 3, t0 + 96, lim, bad, top);
-      const bool move = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
-      if (__any_sync(0xFFFFFFFFu, move)) {
-        const float to = move ? top : m;
+      // one row's need moves the warp's other rows to their maxima too: they need it less often then
+      if (__any_sync(0xFFFFFFFFu, top > m + kSlack || (m == -INFINITY && top > -INFINITY))) {
+        const float to = fmaxf(m, top);
         const float down = m == -INFINITY ? 1.0f : at_ex2(m - to);  // nothing summed yet where m is -inf
         l *= down;
         m = to;
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       }
       // The two warps of a scheduler take turns at the exponentials, so that one group's MMAs run meanwhile.
       if ((g == 1 || i > 0) && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->turn[g][quarter], par ^ (g == 0 ? 1u : 0u), abort_flag))) return false;
-      const float ref = m == -INFINITY ? 0.0f : m;
+      const float ref = m == -INFINITY ? 0.0f : m - kShift;
       // From the last 32 keys down: a chunk's P goes where S has been read already.
       uint32_t pk[16];
       auto full = [&](int h) {
@@ -471,11 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
         if (rr < row_end) {
           float o[32];
 #pragma unroll
-          for (int n = 0; n < 32; ++n) o[n] = any ? __uint_as_float(x[n]) * down : 0.0f;
+          for (int n = 0; n < 32; ++n) o[n] = any ? __uint_as_float(x[n]) * down : 0.0f;  // times 2^kShift
           if (!two && n_kb > 1) {
 #pragma unroll
             for (int n = 0; n < 32; ++n) o[n] = fmaf(osum[(q + n) * kBlk + r], other, o[n]);
           }
+#pragma unroll
+          for (int n = 0; n < 32; ++n) o[n] *= kUnshift;
           uint4* dst = reinterpret_cast<uint4*>(p.out + row * kD + q);
 #pragma unroll
           for (int k = 0; k < 4; ++k)

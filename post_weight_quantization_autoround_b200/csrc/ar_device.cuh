@@ -45,6 +45,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// 2^(127 - code - shift) for an E8M0 code (up to 253) and a shift up to 15; subnormal below 2^-126.
+__device__ __forceinline__ float e8m0_inverse(uint32_t code, int shift) {
+  const int n = 254 - shift - static_cast<int>(min(code, 253u));
+  return __uint_as_float(n > 0 ? static_cast<uint32_t>(n) << 23 : 0x00800000u >> (1 - n));
+}
+
 // ---------------------------------------------------------------------------
 // shared-memory addresses and mbarriers
 // ---------------------------------------------------------------------------

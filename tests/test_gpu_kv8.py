@@ -628,3 +628,93 @@ def test_binding_refusals(ar):
     with pytest.raises(ar.ARError):
         ar.ar_mxfp4_gemm(A, codes[:, :16], scales, torch.empty(3, 8, dtype=torch.bfloat16, device="cuda"))
     assert ar.ar_get_device_status() == ar.AR_OK
+
+
+def _reference64(c, q, n_new, shift):
+    """Outputs and log-sum-exps of a batch of one sequence in 64 bits on the GPU, and the tolerance: an output's bf16 half step; the
+    exponent's error (as in _check) of every weight; a weight's f16 half step, 2^-11 of it or 2^-25 below f16's normal range, with
+    the row's largest weight (times its value scale) at 2^shift."""
+    n, d, group = c.lens[0], c.d, c.n_heads // c.n_kv
+    at = np.arange(n)
+    pg = c.table[0, at // c.page]
+    out, tol = (torch.empty(n_new, c.n_heads, d, dtype=torch.float64, device="cuda") for _ in range(2))
+    lse = torch.empty(n_new, c.n_heads, dtype=torch.float64, device="cuda")
+    x = q[:n_new].double().view(n_new, c.n_heads, d)
+    late = torch.ones(n_new, n, dtype=torch.bool, device="cuda").triu(n - n_new + 1)
+    for h in range(c.n_kv):
+        key = torch.from_numpy(L.e4m3_values(c.k[pg, h, at % c.page]) * np.ldexp(1.0, c.ks[pg, h].astype(int) - 127)[:, None]).cuda()
+        code = torch.from_numpy(L.e4m3_values(c.v[pg, h, at % c.page])).cuda()
+        ev = torch.from_numpy(c.vs[pg, h].astype(np.float64) - 127).cuda()
+        value = code * torch.exp2(ev)[:, None]
+        for i in range(h * group, (h + 1) * group):
+            z = (x[:, i] @ key.t() * d ** -0.5).masked_fill(late, -torch.inf)
+            zerr = 16 * 2.0 ** -23 * (x[:, i].abs() @ key.abs().t()).amax(1) * d ** -0.5 + 2.0 ** -21
+            lse[:, i] = torch.logsumexp(z, 1)
+            p = torch.exp(z - lse[:, i, None])
+            out[:, i] = p @ value
+            u = z / np.log(2) + ev
+            top = u.amax(1, keepdim=True)
+            half = torch.clamp(torch.exp2(u - top + shift) * 2.0 ** -11, min=2.0 ** -25).masked_fill(late, 0.0)
+            unit = torch.exp2(top - shift - lse[:, i, None] / np.log(2))
+            tol[:, i] = 2.0 ** -8 * out[:, i].abs() + 2 * zerr[:, None] * (p @ value.abs()) + (half @ code.abs()) * unit
+    return out, lse, tol
+
+
+def _sink(n, page, raised, n_heads, n_kv, d, n_new, weight):
+    """A cache and queries whose first key takes `weight` of every row and has the value zero, before n - 1 keys of ordinary scores:
+    they make the output.  raised: the first page's value scale is so many powers of two above the others'."""
+    c = Cache([n], n_heads, n_kv, d, page, n_heads)
+    rng = np.random.default_rng(n + n_heads)
+    x = rng.normal(size=c.k.shape)
+    x[..., 0] = 0
+    c.k = L.e4m3_codes(x * 16)
+    c.ks[:] = 127 - 4
+    c.v = L.e4m3_codes((rng.normal(size=c.v.shape) * 0.5 + 1) * 64)
+    c.vs[:] = 127 - 6
+    first = c.table[0, 0]
+    c.k[first, :, 0] = L.e4m3_codes(np.eye(d)[0] * 416)  # 26, the others' dimension 0 is zero
+    c.v[first, :, 0] = 0
+    if raised:
+        c.vs[first] += raised
+        c.v[first] = 0
+    q = rng.normal(size=(n_new, n_heads, d))
+    q[:, :, 0] = np.log(n * np.exp(0.5) * weight / (1 - weight)) * d ** 0.5 / 26
+    return c, torch.from_numpy(q.reshape(n_new, n_heads * d).astype(np.float32)).bfloat16().cuda()
+
+
+def _check_sink(c, q, n_new, out, lse, shift):
+    ref, rl, tol = _reference64(c, q, n_new, shift)
+    err = (out.double().view_as(ref) - ref).abs()
+    assert (err <= tol).all(), ((err / tol).max().item(), (err / ref.abs()).max().item())
+    assert (tol <= 2.0 ** -6 * ref.abs()).all()  # what the test allows is little next to the output
+    assert ((lse.double() - rl).abs() <= 2.0 ** -14 * rl.abs()).all()
+
+
+@pytest.mark.parametrize("weight", [0.99, 0.999])
+@pytest.mark.parametrize("n,page,raised", [(32000, 64, 0), (131000, 128, 0), (32000, 16, 6)])
+@pytest.mark.parametrize("n_heads,n_kv,d,n_new", [(8, 1, 128, 1), (4, 2, 64, 2), (24, 1, 128, 1), (64, 1, 128, 96)])
+def test_attention_sink(ar, n_heads, n_kv, d, n_new, n, page, raised, weight):
+    # raised by more, weights fall below what f16 holds to a bf16 step: by 2^4 earlier on tcgen05
+    c, q = _sink(n, page, min(raised, 2) if n_new == 96 else raised, n_heads, n_kv, d, n_new, weight)
+    cu, cud, ld = _index([n_new], [n])
+    lse = torch.empty(n_new, n_heads, device="cuda")
+    out = _attend(ar, c, q, cud, ld, n_new, lse=lse)
+    tc = "attn_kv8_tc_kernel" in ar.ar_last_kernels()
+    assert tc == (n_new == 96) and ar.ar_get_device_status() == ar.AR_OK
+    _check_sink(c, q, n_new, out, lse, 11 if tc else 15)
+
+
+@pytest.mark.parametrize("weight", [0.99, 0.999])
+def test_attention_sink_of_a_batch(ar, weight):
+    """The same cache read by so many sequences that a warp runs through nearly all of an item's keys."""
+    n, S = 32000, 450
+    c, q = _sink(n, 64, 0, 8, 4, 128, 1, weight)
+    cu, cud, ld = _index([1] * S, [n] * S)
+    lse = torch.empty(S, 8, device="cuda")
+    one = c.table
+    c.table, c.lens = np.repeat(one, S, 0), [n] * S
+    out = _attend(ar, c, q.repeat(S, 1), cud, ld, 1, lse=lse)
+    assert ar.ar_get_device_status() == ar.AR_OK
+    c.table, c.lens = one, [n]
+    for s in range(0, S, 7):
+        _check_sink(c, q, 1, out[s:s + 1], lse[s:s + 1], 15)
