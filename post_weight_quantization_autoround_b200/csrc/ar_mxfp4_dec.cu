@@ -9,7 +9,9 @@
 //    an operand register in one instruction; bf16 operands would take three and a multiply.
 //  * Activations become f16 by a power of two per token and 256 k (largest value in
 //    [2^13, 2^14)): what f16 loses lies 2^-38 below that span's largest value, under the
-//    fp32 sum's own rounding.  The factor goes back on when the span's sum is added.
+//    fp32 sum's own rounding.  The factor goes back on when the span's sum is added.  Where a sum of a span
+//    is not finite before that (scale codes from about 232 on), the span is summed again with a block's scale and its
+//    activations' factor joined (careful_span): the result overflows only where the product does.
 //  * A 32-code block of a row is 16 bytes: lane c of a row's four takes word c, so the two
 //    instructions of a block use 8 consecutive k a lane, activations are one 16-byte load,
 //    and the block's scale multiplies the fp32 sums of exactly that block.
@@ -18,9 +20,9 @@
 //    the activations stays in shared memory; their sums meet through distributed shared
 //    memory.  Parts are added in a fixed order.
 //
-// 5 tokens through 8192 x 28672 (125 MB of codes and scales): 45 us, 2.8 TB/s, 43 % of a copy's
+// 5 tokens through 8192 x 28672 (125 MB of codes and scales): 46 us, 2.7 TB/s, 42 % of a copy's
 // rate; 58 % of the issue slots and 54 % of the integer pipe are busy, about 56 instructions a
-// block and tile, half of them the box's control.  One token 39 us (34 of them the same loop).
+// block and tile, half of them the box's control; 1 us of it looks for sums that are not finite.  One token 39 us (34 of them the same loop).
 // Four CTAs to a cluster instead of two 48 us (132 of 148 SMs hold clusters of four), 8 warps 66 us.
 #include "ar_internal.h"
 
@@ -94,6 +96,62 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// the largest magnitude, NaN if one is
+__device__ __forceinline__ float max_mag4(const float (&x)[4]) {
+  float m;
+  asm("{\n\t.reg .f32 a, b, c, d;\n\tabs.f32 a, %1;\n\tabs.f32 b, %2;\n\tabs.f32 c, %3;\n\tabs.f32 d, %4;\n\t"
+      "max.NaN.f32 a, a, b;\n\tmax.NaN.f32 c, c, d;\n\tmax.NaN.f32 %0, a, c;\n\t}"
+      : "=f"(m)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+  return m;
+}
+
+// x 2^e for |e| <= 254 in two exact steps: an infinity or a lost bit is the product's own
+__device__ __forceinline__ float times_pow2(float x, int e) {
+  const int half = e / 2, rest = e - half;  // -127 .. 127
+  auto pow2 = [](int n) { return __uint_as_float(n > -127 ? static_cast<uint32_t>(n + 127) << 23 : 0x00400000u); };
+  return x * pow2(half) * pow2(rest);
+}
+
+// A warp's unit (16 rows x 256 k) with a power of two per token and block of 32 for the activations, which come from
+// `A` again; a block's scale and its token's factor are one power of two.  Adds to the sums.
+__device__ __noinline__ float4 careful_span(uint32_t w, uint32_t flip, uint2 s0, uint2 s1, const uint16_t* A, int T, int K, int k0,
+                                            float4 tot) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const uint16_t* row = A + static_cast<int64_t>(min(g, T - 1)) * K;
+  const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int b = 0; b < 8; ++b) {
+    const int k = k0 + 32 * b + 8 * c;
+    const uint4 raw = k < K ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t m = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu), __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
+    m = max(m & 0xFFFFu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const int e = min(126, max(-120, 13 + 127 - static_cast<int>(m >> 7)));
+    const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t a[4], h0[4], h1[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = pack_f16x2(bf16_lo(r[j]) * up, bf16_hi(r[j]) * up);
+    const uint32_t off = static_cast<uint32_t>(b << 4) ^ flip;
+    e2m1x8_f16(lds32(w + off), h0);
+    e2m1x8_f16(lds32(w + off + 1024), h1);
+    float d[4];
+    mma_f16(d, h0[0], h1[0], h0[1], h1[1], a[0], a[1], zero);
+    mma_f16(d, h0[2], h1[2], h0[3], h1[3], a[2], a[3], d);
+    const int shift = 8 * (b & 3);
+    const int x0 = static_cast<int>(((b < 4 ? s0.x : s0.y) >> shift) & 0xFFu), x1 = static_cast<int>(((b < 4 ? s1.x : s1.y) >> shift) & 0xFFu);
+    const int ea = __shfl_sync(0xFFFFFFFFu, e, 8 * c) + 127, eb = __shfl_sync(0xFFFFFFFFu, e, 8 * c + 4) + 127;
+    const float nan = __uint_as_float(0x7FC00000u);
+    tot.x += x0 == 255 ? nan : times_pow2(d[0], x0 - ea);
+    tot.y += x0 == 255 ? nan : times_pow2(d[1], x0 - eb);
+    tot.z += x1 == 255 ? nan : times_pow2(d[2], x1 - ea);
+    tot.w += x1 == 255 ? nan : times_pow2(d[3], x1 - eb);
+  }
+  return tot;
 }
 
 template <int CL>
@@ -275,10 +333,18 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
         acc[3] = fmaf(d[3], f1, acc[3]);
       }
       const float2 fa = *reinterpret_cast<const float2*>(factor + sp * 8 + 2 * c);
-      tot[0] = fmaf(acc[0], fa.x, tot[0]);
-      tot[1] = fmaf(acc[1], fa.y, tot[1]);
-      tot[2] = fmaf(acc[2], fa.x, tot[2]);
-      tot[3] = fmaf(acc[3], fa.y, tot[3]);
+      if (__any_sync(0xFFFFFFFFu, !(max_mag4(acc) <= 3.4028235e38f))) {
+        const float4 t = careful_span(w, flip, sc[0], sc[1], p.A, p.T, p.K, (s0 + sp) * kSpan, make_float4(tot[0], tot[1], tot[2], tot[3]));
+        tot[0] = t.x;
+        tot[1] = t.y;
+        tot[2] = t.z;
+        tot[3] = t.w;
+      } else {
+        tot[0] = fmaf(acc[0], fa.x, tot[0]);
+        tot[1] = fmaf(acc[1], fa.y, tot[1]);
+        tot[2] = fmaf(acc[2], fa.x, tot[2]);
+        tot[3] = fmaf(acc[3], fa.y, tot[3]);
+      }
       __syncwarp();  // the slot has been read
       if (next < u1) issue(stage);
       if (++stage == stages) {

@@ -279,3 +279,31 @@ def test_full_size_rows(ar):
         out = _product(ar, A, codes, scales)
         _check_product(out[:, :64], A, codes[:64], scales[:64])
         _check_product(out[:, -64:], A, codes[:64], scales[:64])
+
+
+@pytest.mark.parametrize("K", [256, 1056])
+@pytest.mark.parametrize("T", [1, 5, 8, 9, 40])
+def test_product_large_scales(ar, T, K):
+    """Scale codes up to 252, the largest of finite weights, in some rows, with activations that keep the result finite; a row
+    whose product is not finite, and one whose scale is NaN next to large ones, do not touch the others."""
+    rng = np.random.default_rng(T + K)
+    N = 50
+    codes = torch.from_numpy(rng.integers(0, 256, (N, K // 2), dtype=np.uint8)).cuda()
+    scales = torch.from_numpy(rng.integers(214, 253, (N, K // 32), dtype=np.uint8))
+    scales[::3] = torch.from_numpy(rng.integers(100, 130, (len(range(0, N, 3)), K // 32), dtype=np.uint8))
+    scales[7] = 252
+    scales = scales.cuda()
+    A = (_acts(T, K, 3).double() * 2.0 ** -30).bfloat16()
+    _check_product(_product(ar, A, codes, scales), A, codes, scales)
+    one = torch.zeros_like(A)
+    one[:, 5] = 1.0  # one product a result: exact
+    want = torch.from_numpy(L.mxfp4_values(codes.cpu().numpy(), scales.cpu().numpy())[:, 5]).cuda()
+    assert torch.equal(_product(ar, one, codes, scales).double(), want.expand(T, N))
+    scales[4, 1] = 255
+    big = one * 64.0
+    got = _product(ar, big, codes, scales).double()
+    assert got[:, 4].isnan().all()
+    keep = [n for n in range(N) if n != 4]
+    want = (64.0 * want).bfloat16().double()  # infinite where it leaves the range
+    assert torch.equal(got[:, keep], want[keep].expand(T, N - 1)) and want.isinf().any()
+    assert ar.ar_get_device_status() == ar.AR_OK
