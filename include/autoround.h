@@ -597,7 +597,9 @@ AR_API ar_status ar_kv8_append(const ar_kv8_cfg* cfg, const uint16_t* qkv, int64
  * sequence's new tokens (longer ones are refused on the device).  It and T choose the
  * kernel: at head_dim 128, rows enough to fill tiles of 128 run on tcgen05 (sequences
  * of single tokens next to them on the other kernel, in the same call), else
- * mma.sync with every warp an equal share of all keys.
+ * mma.sync with every warp an equal share of all keys.  What runs on mma.sync is limited to 2^31 steps, else
+ * AR_ERR_UNSUPPORTED (from the workspace query too): n_kv_heads times tiles of rows (rows are new tokens times
+ * n_heads / n_kv_heads, 32 a tile at most) times max_pages * page_size / 16.
  * The result does not depend on timing; the lengths may change between replays
  * of a captured call.  Codes 0x7F and 0xFF (NaN) are not written by ar_kv8_append;
  * places past a sequence's end may hold anything.

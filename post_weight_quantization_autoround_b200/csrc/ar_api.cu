@@ -1295,17 +1295,17 @@ ar_status ar_kv8_append(const ar_kv8_cfg* cfg, const uint16_t* qkv, int64_t T, c
   return end_call();
 }
 
-// the steps that a call can have at most must fit 31 bits
+// the steps that the mma.sync kernel's list can have at most must fit 31 bits
 static ar_status check_kv8_steps(const Kv8Args& a) {
   if (attn_kv8_steps(a) >= 2147483648.0)
-    return fail(AR_ERR_UNSUPPORTED, "too many row tiles times keys for one call: split the batch");
+    return fail(AR_ERR_UNSUPPORTED, "too many row tiles times keys for one call: fewer new tokens or a narrower page_table");
   return AR_OK;
 }
 
 size_t ar_attention_kv8_workspace(const ar_kv8_cfg* cfg, int64_t T, int64_t S, int64_t max_new) {
   begin_call();
   Kv8Args a;
-  if (kv8_args(cfg, T, nullptr, nullptr, nullptr, S, max_new, &a) != AR_OK) return 0;
+  if (kv8_args(cfg, T, nullptr, nullptr, nullptr, S, max_new, &a) != AR_OK || check_kv8_steps(a) != AR_OK) return 0;
   return align_up(attn_kv8_workspace(a), 256);
 }
 

@@ -37,6 +37,8 @@
 // 64 sequences up to 8191 keys, 64 heads over 8 of 128 (572 MB): 115 us for this kernel, 119 with the second,
 // 4.8 TB/s, 75 % of a copy's rate; 2 x 131000 keys 104 us, 5.2 TB/s.  While an SM is busy it takes its share of the
 // full rate, but equal runs end 134 to 170 thousand cycles in: some SMs are served faster than others.
+#include <algorithm>
+
 #include "ar_internal.h"
 
 namespace ar {
@@ -847,9 +849,18 @@ size_t workspace_of() {
 
 }  // namespace
 
-double attn_kv8_steps(const Kv8Args& a) {
-  const int nt = tiles_of(a);
-  const double tiles = static_cast<double>(a.T) * (a.n_heads / a.n_kv) / (8 * nt) + a.S;
+double attn_kv8_steps(const Kv8Args& args) {
+  Kv8Args a = args;
+  double tiles = a.S;  // next to the other kernel: at most a tile of each sequence
+  if (attn_kv8_tc_fits(a)) {
+    a.split_rows = split_rows_of(a);
+    if (a.split_rows == 0) return 0.0;
+  }
+  const int nt = tiles_of(a), rows = 8 * nt, group = a.n_heads / a.n_kv;
+  if (a.split_rows == 0) {
+    const int64_t most = (static_cast<int64_t>(a.max_new) * group + rows - 1) / rows;
+    tiles = std::min(static_cast<double>(a.T) * group / rows + a.S, static_cast<double>(most) * a.S);
+  }
   return tiles * a.n_kv * (static_cast<double>(a.max_pages) * a.page / (nt == 4 ? kBox : 2 * kBox) + 1.0);
 }
 

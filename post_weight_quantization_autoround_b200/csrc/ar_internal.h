@@ -231,7 +231,7 @@ cudaError_t launch_kv8_append(const Kv8Args& a, const uint16_t* qkv, double rope
                               uint8_t* v_pages, uint8_t* k_scales, uint8_t* v_scales, uint16_t* q_out,
                               cudaStream_t stream);
 size_t attn_kv8_workspace(const Kv8Args& a);
-double attn_kv8_steps(const Kv8Args& a);  // an upper bound of a call's work, in steps
+double attn_kv8_steps(const Kv8Args& a);  // an upper bound of the steps that a call's mma.sync kernel lists; 0: it has none
 cudaError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, float sm_scale, const uint8_t* k_pages,
                             const uint8_t* v_pages, const uint8_t* k_scales, const uint8_t* v_scales, uint16_t* out,
                             float* lse, void* workspace, cudaStream_t stream);

@@ -8,6 +8,8 @@ within half a step (2^-4 relative, 2^-10 of the scale for subnormal codes) plus 
 Attention: P is f16 (2^-11 relative half a step, 2^-25 absolute where it is subnormal), the exponent carries fp32
 errors of z: sums over d / 16 steps and the scaling, at most 16 * 2^-23 of the largest sum of magnitudes, times ln 2
 by the exponential (2^-22 more); the output rounds to bf16 (2^-8)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -718,3 +720,32 @@ def test_attention_sink_of_a_batch(ar, weight):
     c.table, c.lens = one, [n]
     for s in range(0, S, 7):
         _check_sink(c, q, 1, out[s:s + 1], lse[s:s + 1], 15)
+
+
+@pytest.mark.parametrize("T,S,max_new,max_pages", [
+    (131072, 1, 131072, 1024),  # a prompt of 131072 tokens
+    (16384, 1, 16384, 1 << 13),  # a piece of a prompt, a page table of 2^20 tokens
+    (32768, 4, 20000, 1 << 13),
+    (16384 + 63, 64, 16384, 1 << 13),  # next to 63 single tokens
+])
+def test_attention_steps_do_not_bound_prompts(ar, T, S, max_new, max_pages):
+    """The limit of mma.sync's list of steps is not a limit of what runs on tcgen05: the sizes pass the checks (the workspace's,
+    which follows, refuses the call: nothing runs)."""
+    assert ar.ar_attention_kv8_workspace(T, S, max_new, 64, 8, 128, 128, 1000, max_pages) > 0
+    cfg, p = ar.Kv8Cfg(64, 8, 128, 128, 1000, max_pages), 0x100000
+    st = ar.lib().ar_attention_kv8(ctypes.byref(cfg), p, T, p, p, p, S, max_new, 0.0, p, p, p, p, p, None, None, 0, None)
+    assert st == ar.AR_ERR_WORKSPACE, ar.ar_last_error()
+
+
+def test_attention_long_prompt(ar):
+    """A whole prompt whose row tiles times the page table's width pass 2^31, on tcgen05; sampled rows of it."""
+    n, n_heads, n_kv, d, page = 32768, 64, 8, 128, 128
+    c = Cache([n], n_heads, n_kv, d, page, 2, garbage=False, max_pages=(1 << 20) // page)
+    cu, cud, ld = _index([n], [n])
+    q = torch.randn(n, n_heads * d, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).bfloat16()
+    out = _attend(ar, c, q, cud, ld, n)
+    assert ar.ar_last_kernels() == "attn_kv8_tc_kernel" and ar.ar_get_device_status() == ar.AR_OK
+    for t in (0, 1, 127, 128, 4095, 20001, n - 1):
+        c.lens = [t + 1]
+        ref, _, tol = _reference64(c, q[t:t + 1], 1, 11)
+        assert ((out[t].double().view_as(ref) - ref).abs() <= tol).all()

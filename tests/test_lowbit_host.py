@@ -119,3 +119,18 @@ def test_attention_workspace():
     assert 0 < one < many
     with pytest.raises(ar.ARError):
         ar.ar_attention_kv8_workspace(4, 4, 1, **dict(args, head_dim=80))
+
+
+def test_attention_limit_of_steps():
+    """2^31 steps bound what runs on mma.sync; the call and its workspace query agree."""
+    def check(T, S, max_new, refused, **kw):
+        d = dict(n_heads=64, n_kv_heads=8, head_dim=64, page_size=128, n_pages=1000, max_pages=1024)
+        d.update(kw)
+        got = attend(cfg8(**d), T=T, S=S, max_new=max_new, ws=None)
+        size = ar.lib().ar_attention_kv8_workspace(ctypes.byref(cfg8(**d)), T, S, max_new)
+        assert (got, size > 0) == ((NO, False) if refused else (WS, True)), (got, size, ar.ar_last_error())
+
+    check(65536, 1, 65536, False)
+    check(1 << 20, 64, 1, False, max_pages=1 << 13)  # rows behind the last sequence are no work
+    check(131072, 1, 131072, True)
+    check(4096, 4096, 1, True, head_dim=128, max_pages=1 << 23)
