@@ -189,7 +189,7 @@ __device__ __forceinline__ void write_row(const AttnParams& p, const Seq& seq, i
   const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
   *reinterpret_cast<uint2*>(p.out + row * D + d) =
       make_uint2(pack_bf16x2(acc.x * kUnshift * inv, acc.y * kUnshift * inv), pack_bf16x2(acc.z * kUnshift * inv, acc.w * kUnshift * inv));
-  if (p.lse && d == 0) p.lse[row] = sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  if (p.lse && d == 0) p.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;  // a NaN stays one
 }
 
 // where a warp's run of steps stands
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
               *reinterpret_cast<uint32_t*>(p.out + row * D + 16 * mt + 2 * g) =
                   pack_bf16x2(o[mt][nt][j] * kUnshift * inv, o[mt][nt][2 + j] * kUnshift * inv);
             if (p.lse && g == 0)
-              p.lse[row] = l[nt][j] > 0.0f ? (m[nt][j] + log2f(l[nt][j])) * 0.6931471805599453f : -INFINITY;
+              p.lse[row] = l[nt][j] == 0.0f ? -INFINITY : (m[nt][j] + log2f(l[nt][j])) * 0.6931471805599453f;
           }
       } else {
         const int k = t_first == 0 ? 1 : 0;

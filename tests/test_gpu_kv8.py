@@ -749,3 +749,23 @@ def test_attention_long_prompt(ar):
         c.lens = [t + 1]
         ref, _, tol = _reference64(c, q[t:t + 1], 1, 11)
         assert ((out[t].double().view_as(ref) - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("n_heads,n_kv,d,n_new,lens", [(8, 1, 128, 1, [60, 70]), (8, 2, 64, 1, [30000, 9]), (64, 8, 128, 200, [400, 333])])
+def test_attention_lse_of_a_nan_row(ar, n_heads, n_kv, d, n_new, lens):
+    """Rows without keys have a log-sum-exp of -inf; a row whose query is NaN has NaN, in one warp's item, in one that blocks
+    share, and on tcgen05."""
+    c = Cache(lens, n_heads, n_kv, d, 32, 2)
+    cu, cud, ld = _index([n_new] * 2, lens)
+    q = torch.from_numpy(c.rng.normal(size=(2 * n_new, n_heads * d)).astype(np.float32)).bfloat16().cuda()
+    want = torch.empty(2 * n_new, n_heads, device="cuda")
+    _attend(ar, c, q, cud, ld, n_new, lse=want)
+    rows = [(0, 1), (n_new, n_heads - 1), (2 * n_new - 1, 0)]
+    for t, h in rows:
+        q[t, h * d + 7] = float("nan")
+    lse = torch.empty_like(want)
+    out = _attend(ar, c, q, cud, ld, n_new, lse=lse)
+    for t, h in rows:
+        assert lse[t, h].isnan() and out[t, h * d:(h + 1) * d].isnan().all()
+        lse[t, h] = want[t, h]
+    assert torch.equal(lse, want)
