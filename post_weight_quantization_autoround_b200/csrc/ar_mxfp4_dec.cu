@@ -8,10 +8,12 @@
 //    f16 in and fp32 out.  E2M1 is a subset of f16 and the hardware converts two codes to
 //    an operand register in one instruction; bf16 operands would take three and a multiply.
 //  * Activations become f16 by a power of two per token and 256 k (largest value in
-//    [2^13, 2^14)): what f16 loses lies 2^-38 below that span's largest value, under the
-//    fp32 sum's own rounding.  The factor goes back on when the span's sum is added.  Where a sum of a span
-//    is not finite before that (scale codes from about 232 on), the span is summed again with a block's scale and its
-//    activations' factor joined (careful_span): the result overflows only where the product does.
+//    [2^13, 2^14)): what f16 loses lies 2^-38 below that span's largest value.  The factor goes
+//    back on when the span's sum is added.  Two kinds of span are summed again with a power of two per
+//    token and block of 32, joined with the block's scale (careful_span): where a sum is not finite before
+//    the factor (scale codes from about 232 on), so that the result overflows only where the product does; and
+//    where a block's largest activation lies more than 2^16 below the span's, since the block's scale may
+//    make up for it.  A block so loses 2^-22 of its largest activation at most, as much as the fp32 sum rounds.
 //  * A 32-code block of a row is 16 bytes: lane c of a row's four takes word c, so the two
 //    instructions of a block use 8 consecutive k a lane, activations are one 16-byte load,
 //    and the block's scale multiplies the fp32 sums of exactly that block.
@@ -40,6 +42,7 @@ constexpr int kSlots = kPassTiles + kWarps;  // (tile, warp) pairs along the war
 constexpr int kRingBytes = kWarps * kBoxBytes;  // per stage
 constexpr int kFixedBytes = (kSlots + kPassTiles) * 128 * 4 + 1024 + 1024;  // slots, sums, barriers, alignment
 constexpr int kSmemMax = 226 * 1024;
+constexpr uint32_t kFarBlock = 16;  // binary places that a block's activations may lie below the span's
 constexpr int kActBytesMax = kSmemMax - kFixedBytes - 2 * kRingBytes;
 
 struct DecCtl {
@@ -233,8 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
           uint32_t m = __vmaxu2(__vmaxu2(raw[b].x & 0x7FFF7FFFu, raw[b].y & 0x7FFF7FFFu),
                                 __vmaxu2(raw[b].z & 0x7FFF7FFFu, raw[b].w & 0x7FFF7FFFu));
           m = max(m & 0xFFFFu, m >> 16);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          const uint32_t block = m;  // four lanes hold a block of 32
+          m = __reduce_max_sync(0xFFFFFFFFu, m);
+          const bool far = __any_sync(0xFFFFFFFFu, block != 0u && (m >> 7) - (block >> 7) > kFarBlock);
           if (i >= items) continue;
           const int e = min(126, max(-120, 13 + 127 - static_cast<int>(m >> 7)));
           const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
@@ -244,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
           for (int j = 0; j < 4; ++j) h[j] = pack_f16x2(bf16_lo(r[j]) * up, bf16_hi(r[j]) * up);
           *reinterpret_cast<uint4*>(act + ((sp * 8 + (lane >> 2)) * p.T + t) * 64 + (lane & 3) * 16) =
               make_uint4(h[0], h[1], h[2], h[3]);
-          if (lane == 0) factor[sp * 8 + t] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          if (lane == 0) factor[sp * 8 + t] = (far ? -1.0f : 1.0f) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // negative: careful_span
         }
       }
       // columns past the last token: a factor that keeps their sums finite
@@ -333,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_dec_kernel(const __grid_con
         acc[3] = fmaf(d[3], f1, acc[3]);
       }
       const float2 fa = *reinterpret_cast<const float2*>(factor + sp * 8 + 2 * c);
-      if (__any_sync(0xFFFFFFFFu, !(max_mag4(acc) <= 3.4028235e38f))) {
+      if (__any_sync(0xFFFFFFFFu, !(max_mag4(acc) <= 3.4028235e38f) || fminf(fa.x, fa.y) < 0.0f)) {
         const float4 t = careful_span(w, flip, sc[0], sc[1], p.A, p.T, p.K, (s0 + sp) * kSpan, make_float4(tot[0], tot[1], tot[2], tot[3]));
         tot[0] = t.x;
         tot[1] = t.y;

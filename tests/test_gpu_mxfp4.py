@@ -307,3 +307,28 @@ def test_product_large_scales(ar, T, K):
     want = (64.0 * want).bfloat16().double()  # infinite where it leaves the range
     assert torch.equal(got[:, keep], want[keep].expand(T, N - 1)) and want.isinf().any()
     assert ar.ar_get_device_status() == ar.AR_OK
+
+
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9])
+@pytest.mark.parametrize("K", [256, 800])
+def test_product_scales_that_make_up_for_activations(ar, T, K):
+    """Blocks whose activations lie far below the others' (2^-16 to 2^-60 of the largest) and whose weights' scales are as much
+    larger: each block counts as much as the others.  A token whose activations are all alike next to it, and blocks of
+    zeros."""
+    rng = np.random.default_rng(T + K)
+    N = 40
+    down = rng.permutation(np.linspace(0, 60, K // 32).round().astype(int))
+    codes = torch.from_numpy(rng.integers(0, 256, (N, K // 2), dtype=np.uint8)).cuda()
+    scales = torch.from_numpy(np.broadcast_to(down + 120, (N, K // 32)).astype(np.uint8).copy())
+    scales[N // 2:] = 127
+    scales = scales.cuda()
+    A = rng.normal(size=(T, K)) * np.repeat(2.0 ** -down.astype(float), 32)[None]
+    A[:, :32] = 0
+    if T > 2:
+        A[1] = rng.normal(size=K)
+    A = torch.from_numpy(A).bfloat16().cuda()
+    _check_product(_product(ar, A, codes, scales), A, codes, scales)
+    # without the largest block the others still come out to the product's own rounding
+    A[:, torch.from_numpy(np.repeat(down == 0, 32))] = 0
+    _check_product(_product(ar, A, codes, scales), A, codes, scales)
+    assert ar.ar_get_device_status() == ar.AR_OK
