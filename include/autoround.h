@@ -603,7 +603,8 @@ AR_API ar_status ar_kv8_append(const ar_kv8_cfg* cfg, const uint16_t* qkv, int64
  * The result does not depend on timing; the lengths may change between replays
  * of a captured call.  Codes 0x7F and 0xFF (NaN) are not written by ar_kv8_append;
  * places past a sequence's end may hold anything.
- * Scores, maxima and row sums are fp32.  A weight enters the sum of the values in f16: off by 2^-11 of itself
+ * Scores are fp32 sums of the codes and of the queries in f16 by a power of two per row (off by 2^-38 of the row's
+ * largest value at most); maxima and row sums are fp32, whatever the value scales.  A weight enters the sum of the values in f16: off by 2^-11 of itself
  * at most, or, where that is more, by 2^-36 of the row's largest weight times its value scale.
  * workspace: ar_attention_kv8_workspace bytes (device, 256-byte aligned); calls that
  * overlap on the GPU need one each. */

@@ -19,7 +19,9 @@
 //    product: off by 2^-11 of itself at most (finer than the bf16 output) down to 2^-29 of the row's
 //    largest, and by 2^-40 of that below, which is why its range is used up to 2^15: behind a key
 //    that takes nearly all weight and has a small value, 10^5 keys still count.  The row sum takes the
-//    fp32 value; maximum, sum and O are fp32.
+//    fp32 value; maximum, sum and O are fp32.  Where a page's value scale lies so far below the others' (a
+//    page of zeros next to large values) that P' itself would leave fp32, the row sum takes those weights in a
+//    second look, and sums move to a new maximum in two factors.
 //  * S^T leaves the tensor core with tokens along lanes' rows; movmatrix transposes the
 //    8 x 8 blocks into the B operand of O^T.  V^T comes from ldmatrix.trans on byte pairs:
 //    one byte permute separates even and odd dimensions.
@@ -547,9 +549,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float mn = fmaxf(m[nt][j], top[j]);
-            sc[j] = mn == -INFINITY ? 1.0f : ex2(m[nt][j] - mn);
+            const float half = mn == -INFINITY ? 1.0f : ex2(0.5f * (m[nt][j] - mn));
+            sc[j] = half * half;
             m[nt][j] = mn;
-            l[nt][j] *= sc[j];
+            l[nt][j] = l[nt][j] * half * half;
           }
 #pragma unroll
           for (int mt = 0; mt < kMt; ++mt) {
@@ -571,6 +574,19 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
           }
           pb[nt][h][0] = movmatrix(pack_f16x2(pr[0], pr[1]));
           pb[nt][h][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
+        }
+        // Weights that went to zero (below 2^-126) count where 2^30 of them could be 2^-24 of the row's sum.
+        float low = back[0];
+        if (kHalves == 2) low = fmaxf(low, back[kHalves - 1]);
+        low *= 0x1p-72f;
+        if (__any_sync(0xFFFFFFFFu, (l[nt][0] < low && lim[nt][0] > 0) || (l[nt][1] < low && lim[nt][1] > 0))) {
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x = z[nt][h][j] - base[j & 1];
+              if (x < -126.0f) l[nt][j & 1] = fmaf(ex2(x + 126.0f), back[h] * 0x1p-126f, l[nt][j & 1]);
+            }
         }
       }
 
@@ -707,8 +723,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kBlo
       for (int j = 0; j < kWarps; ++j) mx = fmaxf(mx, ml[j].x);
 #pragma unroll
       for (int j = 0; j < kWarps; ++j) {
-        const float f = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - mx);
-        sum = fmaf(ml[j].y, f, sum);
+        const float half = ml[j].x == -INFINITY ? 0.0f : ex2(0.5f * (ml[j].x - mx)), f = half * half;
+        sum = fmaf(ml[j].y * half, half, sum);
         acc.x = fmaf(x[j].x, f, acc.x);
         acc.y = fmaf(x[j].y, f, acc.y);
         acc.z = fmaf(x[j].z, f, acc.z);
@@ -770,8 +786,8 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(const AttnParams p) 
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const float f = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - mx);
-        sum = fmaf(ml[j].y, f, sum);
+        const float half = ml[j].x == -INFINITY ? 0.0f : ex2(0.5f * (ml[j].x - mx)), f = half * half;
+        sum = fmaf(ml[j].y * half, half, sum);
         acc.x = fmaf(x[j].x, f, acc.x);
         acc.y = fmaf(x[j].y, f, acc.y);
         acc.z = fmaf(x[j].z, f, acc.z);

@@ -16,7 +16,8 @@
 //    memory, which few blocks need after the first.  P' reaches 2^15 there, and 2^11 at a reference that
 //    stays, so f16 is off by 2^-11 of a weight, or by 2^-36 of the row's largest where that is more (behind a
 //    key that takes nearly all weight and has a small value the others count all the same).  A wider margin
-//    leaves less below: 2^8 took 144 us where 2^4 takes 148 and 2^2 152 (the case below).
+//    leaves less below: 2^8 took 144 us where 2^4 takes 148 and 2^2 152 (the case below).  A block with a
+//    value scale 2^80 below another's has a second look at the weights that left fp32 (kFarCodes).
 //  * 10-13: expansion.  Codes come straight from the pages to registers a block ahead, each
 //    conversion instruction makes two f16, and the tile is written as the MMAs read it (128-byte
 //    swizzle; the same layout serves K as the K-major and V as the MN-major operand).
@@ -24,8 +25,8 @@
 // A tile's block of 128 keys costs 1024 cycles of MMAs and the same of exponentials (16 a cycle and SM).
 // The two groups take turns at the exponentials, so that one's MMAs run under the other's; left alone they
 // fall into step and both wait (184 us for the case below, 168 with the turns; 149 with two loads of S in
-// flight and a chunk kept for the second reading).  2 x 512 new tokens of 4000, 64 heads over 8: 148 us
-// in a loop of calls, 553 TFLOP/s.  Of a group's 4800 cycles a block the scores take a quarter, the maximum an eighth,
+// flight and a chunk kept for the second reading).  2 x 512 new tokens of 4000, 64 heads over 8: 149 us
+// in a loop of calls, 549 TFLOP/s.  Of a group's 4800 cycles a block the scores take a quarter, the maximum an eighth,
 // the exponentials two fifths: shared memory, which the MMAs read at its full rate, slows all that
 // goes through it.  One tile a CTA with sixteen softmax warps took 199 us, the mma.sync kernel 587 us; the
 // scores held in registers (168 a thread, MMAs issued by a softmax warp) 204 us, two threads a row 188 us.
@@ -55,6 +56,9 @@ constexpr uint32_t kColP = kColS + kBlk / 2;
 constexpr int kSlack = 4;                 // a block's maximum may pass the reference by 2^4
 constexpr int kShift = 15 - kSlack;       // P' at the reference; the largest is 2^15
 constexpr float kUnshift = 1.0f / (1 << kShift);
+// Where a group's value scale lies 2^80 below another's that the row has seen, weights below 2^-126 count for the row sum:
+// 2^30 of them could be more than 2^-24 of it.
+constexpr uint32_t kFarCodes = 80;
 constexpr int kRowStep = kExThreads / 8;
 constexpr int kRowsPerThread = kBlk / kRowStep;  // 16-byte pieces of a tile a thread expands
 
@@ -109,6 +113,17 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// 16 columns, waited for
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
@@ -342,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
     const float fac = ctl->fac[(two ? g * kBlk : 0) + r];
     float m = -INFINITY, l = 0.0f;
     int i = 0;
-    auto block = [&](auto mask, uint32_t ek, uint32_t ev, uint32_t bad) {
+    uint32_t ev_top = 0;  // largest value scale code so far
+    auto block = [&](auto mask, uint32_t ek, uint32_t ev, uint32_t bad, uint32_t far) {
       constexpr bool kMask = decltype(mask)::value;
       const uint32_t par = static_cast<uint32_t>(i) & 1u;
       Scales c;
@@ -369,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       // one row's need moves the warp's other rows to their maxima too: they need it less often then
       if (__any_sync(0xFFFFFFFFu, top > m + kSlack || (m == -INFINITY && top > -INFINITY))) {
         const float to = fmaxf(m, top);
-        const float down = m == -INFINITY ? 1.0f : at_ex2(m - to);  // nothing summed yet where m is -inf
-        l *= down;
+        const float half = m == -INFINITY ? 1.0f : at_ex2(0.5f * (m - to)), down = half * half;  // nothing summed yet where m is -inf
+        l = l * half * half;
         m = to;
         if (i > 0) {  // O holds the blocks before: S came after the last of their products
 #pragma unroll 1
@@ -391,6 +407,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       // The two warps of a scheduler take turns at the exponentials, so that one group's MMAs run meanwhile.
       if ((g == 1 || i > 0) && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->turn[g][quarter], par ^ (g == 0 ? 1u : 0u), abort_flag))) return false;
       const float ref = m == -INFINITY ? 0.0f : m - kShift;
+      if (kMask && far != 0u) {  // before P overwrites S
+#pragma unroll 1
+        for (int h = 0; h < kGroups; ++h) {
+          if (!((far >> h) & 1)) continue;
+          uint32_t x[16];
+          ld16(col_s + 16 * h, x);
+          const float f = fac * of_group(c.f, h), fe = of_group(c.fe, h) - ref, back = of_group(c.back, h);
+          float low = 0.0f;
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const float d = fmaf(__uint_as_float(x[n]), f, fe);
+            if (t0 + 16 * h + n < lim && d < -126.0f) low += at_ex2(d + 126.0f);
+          }
+          l = fmaf(low, back * 0x1p-126f, l);
+        }
+      }
       // From the last 32 keys down: a chunk's P goes where S has been read already.
       uint32_t pk[16];
       auto full = [&](int h) {
@@ -419,13 +451,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
     for (; ok && j < n_kb; j += step, ++i) {
       const uint32_t ek = ek_next, ev = ev_next;
       const uint32_t bad = __ballot_sync(0xFFFFFFFFu, lane < kGroups && (pg < 0 || pg >= a.n_pages));  // nothing of these
+      // lanes without a group, and groups past the keys or of a page that is not in the pool, have no scale
+      const uint32_t code = lane < kGroups && !((bad >> lane) & 1) ? ev : 0u;
+      ev_top = max(ev_top, __reduce_max_sync(0xFFFFFFFFu, code));
+      const uint32_t far = __ballot_sync(0xFFFFFFFFu, code != 0u && code + kFarCodes < ev_top);
       pg = pg_next;
       scales_of(pg);
       pg_next = page_of(j + 2 * step);
-      if ((j + 1) * kBlk > full_below || bad != 0)
-        ok = block(std::true_type{}, ek, ev, bad);
+      if ((j + 1) * kBlk > full_below || bad != 0 || far != 0)
+        ok = block(std::true_type{}, ek, ev, bad, far);
       else
-        ok = block(std::false_type{}, ek, ev, 0u);
+        ok = block(std::false_type{}, ek, ev, 0u, 0u);
     }
     const bool any = i > 0;  // O has been written
     ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->done[g], 0, abort_flag));
@@ -452,9 +488,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_tc_kernel(const Params p
       at_bar_sync(1, kSmWarps * 32);
       if (g == 0 && *abort_flag == 0) {
         const float m1 = ctl->join[0][r], top = fmaxf(m, m1);
-        down = m == -INFINITY ? 1.0f : at_ex2(m - top);
-        other = m1 == -INFINITY ? 1.0f : at_ex2(m1 - top);
-        l = l * down + ctl->join[1][r] * other;
+        const float half0 = m == -INFINITY ? 1.0f : at_ex2(0.5f * (m - top)), half1 = m1 == -INFINITY ? 1.0f : at_ex2(0.5f * (m1 - top));
+        down = half0 * half0;
+        other = half1 * half1;
+        l = l * half0 * half0 + ctl->join[1][r] * half1 * half1;
         m = top;
       } else {
         ok = ok && g == 0;

@@ -769,3 +769,35 @@ def test_attention_lse_of_a_nan_row(ar, n_heads, n_kv, d, n_new, lens):
         assert lse[t, h].isnan() and out[t, h * d:(h + 1) * d].isnan().all()
         lse[t, h] = want[t, h]
     assert torch.equal(lse, want)
+
+
+@pytest.mark.parametrize("top", [-4, 12, 45, 90, 115])
+@pytest.mark.parametrize("order", ["zeros first", "zeros last", "between"])
+@pytest.mark.parametrize("n_heads,n_kv,d,n_new,n,page", [(8, 2, 128, 1, 70, 16), (4, 2, 64, 1, 300, 32), (24, 1, 128, 1, 9000, 16), (32, 1, 64, 2, 500, 64),
+                                                         (64, 2, 128, 160, 700, 16), (64, 4, 128, 2, 600, 128)])
+def test_attention_pages_of_zeros_next_to_large_values(ar, n_heads, n_kv, d, n_new, n, page, order, top):
+    """Pages of zero values, whose scale is the smallest there is, in front of, behind and between pages of large ones: their
+    keys count in the row sum."""
+    c = Cache([n], n_heads, n_kv, d, page, n + top)
+    pages = -(-n // page)
+    zero = {"zeros first": lambda i: i < pages // 2, "zeros last": lambda i: i >= pages // 2, "between": lambda i: i % 3 == 1}[order]
+    c.ks[:] = 127 - 7
+    for i in range(pages):
+        pg = c.table[0, i]
+        c.vs[pg] = 127 - 100 if zero(i) else 127 + top - i % 2
+        if zero(i):
+            c.v[pg] = 0
+        else:
+            c.v[pg] = L.e4m3_codes(c.rng.uniform(1, 16, c.v[pg].shape))
+    if n % page:
+        c.v[c.table[0, pages - 1], :, n % page:] = 0x7F
+    q = torch.from_numpy(c.rng.normal(size=(n_new, n_heads * d)).astype(np.float32)).bfloat16().cuda()
+    q[0] = 0  # all keys alike
+    cu, cud, ld = _index([n_new], [n])
+    lse = torch.empty(n_new, n_heads, device="cuda")
+    out = _attend(ar, c, q, cud, ld, n_new, lse=lse)
+    assert ("attn_kv8_tc_kernel" in ar.ar_last_kernels()) == (n_new == 160) and ar.ar_get_device_status() == ar.AR_OK
+    ref, rl, tol = _reference64(c, q, n_new, 11 if n_new == 160 else 15)
+    got = out.double().view_as(ref)
+    assert ((got - ref).abs() <= tol).all(), (((got - ref).abs() / tol).max().item(), got[0, 0, :3], ref[0, 0, :3])
+    assert ((lse.double() - rl).abs() <= 2.0 ** -14 * (1 + rl.abs())).all()
