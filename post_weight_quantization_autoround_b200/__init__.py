@@ -552,6 +552,15 @@ def _typed(t: Optional[torch.Tensor], dtype, shape, name: str, device: int) -> O
     return t.data_ptr()
 
 
+def _space(workspace: Optional[torch.Tensor], device: int):
+    """Address and bytes of a workspace on the given (current) device; (None, 0) without one."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ARError(AR_ERR_INVALID_ARG, f"workspace must be a contiguous tensor on the current CUDA device, got one on {workspace.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def ar_qdq_mxfp4(W, V=None, alpha=None, W_hat=None, codes=None, scales=None, stream=None) -> None:
     """MXFP4 fake quantization of W [N][K] (bf16): V [N][K] fp32 or None, alpha [N][K/32] fp32 or None; outputs
     W_hat bf16 [N][K], codes uint8 [N][K/2], scales uint8 [N][K/32] (E8M0 codes), each optional."""
@@ -596,8 +605,8 @@ def ar_tune_step_mxfp4(W, V, alpha, X, Y, cfg: QConfig, n_steps: int, loss_per_s
                                     ctypes.byref(cfg), n_steps,
                                     _typed(loss_per_step, torch.float32, (max(n_steps, 1),), "loss_per_step", dev),
                                     _typed(dV, torch.float32, (N, K), "dV", dev),
-                                    _typed(dalpha, torch.float32, (N, K // 32), "dalpha", dev), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+                                    _typed(dalpha, torch.float32, (N, K // 32), "dalpha", dev), *_space(workspace, dev),
+                                    _stream(stream)))
 
 
 def ar_mxfp4_gemm_workspace(T: int, N: int, K: int) -> int:
@@ -615,9 +624,7 @@ def ar_mxfp4_gemm(A, codes, scales, out, workspace=None, stream=None) -> None:
     dev = torch.cuda.current_device()
     _check(lib().ar_mxfp4_gemm(_typed(A, torch.bfloat16, (T, K), "A", dev), T, _typed(codes, torch.uint8, (N, K // 2), "codes", dev),
                                _typed(scales, torch.uint8, (N, K // 32), "scales", dev), N, K,
-                               _typed(out, torch.bfloat16, (T, N), "out", dev), _ptr(workspace),
-                               0 if workspace is None else workspace.numel() * workspace.element_size(),
-                               _stream(stream)))
+                               _typed(out, torch.bfloat16, (T, N), "out", dev), *_space(workspace, dev), _stream(stream)))
 
 
 # ---- the paged 8-bit cache ----------------------------------------------------
@@ -672,5 +679,5 @@ def ar_attention_kv8(q, cu_seqlens, seq_lens, page_table, k_pages, v_pages, k_sc
     shape = (T, n_heads * k_pages.shape[3])
     _check(lib().ar_attention_kv8(ctypes.byref(cfg), _typed(q, torch.bfloat16, shape, "q", dev), T, *index, S, max_new,
                                   sm_scale, *cache, _typed(out, torch.bfloat16, shape, "out", dev),
-                                  _typed(lse, torch.float32, (T, n_heads), "lse", dev), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+                                  _typed(lse, torch.float32, (T, n_heads), "lse", dev), *_space(workspace, dev),
+                                  _stream(stream)))

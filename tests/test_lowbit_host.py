@@ -3,6 +3,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 import post_weight_quantization_autoround_b200 as ar
 
@@ -134,3 +135,40 @@ def test_attention_limit_of_steps():
     check(1 << 20, 64, 1, False, max_pages=1 << 13)  # rows behind the last sequence are no work
     check(131072, 1, 131072, True)
     check(4096, 4096, 1, True, head_dim=128, max_pages=1 << 23)
+
+
+class _OnDevice(torch.Tensor):
+    """A tensor that says it lies on a CUDA device of the given number."""
+    def get_device(self):
+        return self.number
+
+
+def test_workspace_on_another_device_is_refused():
+    w = torch.empty(64, dtype=torch.float32).as_subclass(_OnDevice)
+    w.number = 1
+    assert ar._space(w, 1) == (w.data_ptr(), 256) and ar._space(None, 0) == (None, 0)
+    with pytest.raises(ar.ARError):
+        ar._space(w, 0)
+    with pytest.raises(ar.ARError):
+        ar._space(torch.empty(64), 0)  # host memory
+    strided = w[::2]
+    strided.number = 1
+    with pytest.raises(ar.ARError):
+        ar._space(strided, 1)
+
+
+def test_entry_points_check_their_workspace(monkeypatch):
+    """Each of the three binds its workspace through that check."""
+    monkeypatch.setattr(ar, "_typed", lambda *a: P)
+    monkeypatch.setattr(ar, "_stream", lambda s: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    w = torch.empty(1 << 20, dtype=torch.uint8).as_subclass(_OnDevice)
+    w.number = 1
+    bf, u8, i32, f32 = (lambda *s, t=t: torch.empty(s, dtype=t) for t in (torch.bfloat16, torch.uint8, torch.int32, torch.float32))
+    calls = [lambda: ar.ar_mxfp4_gemm(bf(4, 64), u8(8, 32), u8(8, 2), bf(4, 8), w),
+             lambda: ar.ar_tune_step_mxfp4(bf(8, 64), f32(8, 64), f32(8, 2), bf(8, 64), f32(8, 8), ar.ar_qconfig_default(), 1, f32(1), w),
+             lambda: ar.ar_attention_kv8(bf(1, 128), i32(2), i32(1), i32(1, 1), u8(1, 1, 16, 128), u8(1, 1, 16, 128), u8(1, 1), u8(1, 1),
+                                         bf(1, 128), 1, w)]
+    for call in calls:
+        with pytest.raises(ar.ARError, match="workspace"):
+            call()
