@@ -1189,7 +1189,8 @@ ar_status ar_tune_step_mxfp4(const uint16_t* W, float* V, float* alpha, int64_t 
 // Where the product expands the weights to bf16 once (the caller's workspace) and runs the pair GEMM, which
 // overlaps its tiles' ends with the next tiles; the GEMM that expands on the way does not, and a short K has
 // many ends.  Measured (us, expanding first / on the way): 11008 x 4096 at 1024 tokens 134 / 121, at 2048
-// 186 / 197, at 4096 327 / 372; 8192 x 28672 at 2048 808 / 747, at 4096 1436 / 1394.
+// 186 / 197, at 4096 327 / 372; 8192 x 28672 at 2048 808 / 747, at 4096 1436 / 1394.  The limits lie at or between
+// these sizes: no other K, N or T was measured.
 static bool mxfp4_expands(int64_t T, int64_t N, int64_t K) { return T >= 2048 && N % 8 == 0 && K <= 8192; }
 
 size_t ar_mxfp4_gemm_workspace(int64_t T, int64_t N, int64_t K) {

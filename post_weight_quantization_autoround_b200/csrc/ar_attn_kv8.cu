@@ -36,8 +36,8 @@
 //    block's run, and by a second kernel where several blocks share it; always in the
 //    order of the tokens: no atomics, the same result every time.
 //
-// 64 sequences up to 8191 keys, 64 heads over 8 of 128 (572 MB): 115 us for this kernel, 119 with the second,
-// 4.8 TB/s, 75 % of a copy's rate; 2 x 131000 keys 104 us, 5.2 TB/s.  While an SM is busy it takes its share of the
+// 64 sequences up to 8191 keys, 64 heads over 8 of 128 (572 MB): 114 us for this kernel, 120 with the second,
+// 4.8 TB/s, 74 % of a copy's rate; 2 x 131000 keys 107 us, 5.0 TB/s.  While an SM is busy it takes its share of the
 // full rate, but equal runs end 134 to 170 thousand cycles in: some SMs are served faster than others.
 #include <algorithm>
 
@@ -806,8 +806,8 @@ int tiles_of(const Kv8Args& a) {
 
 // Where a call that goes to tcgen05 seems to have short sequences too (prompts next to single tokens), those with no
 // more rows than the smallest tile here that holds one token run here, where a long cache is split over the GPU; a
-// tile of the other kernel stays with one SM.  512 new tokens of 4000 next to 31 single ones of 32000, 64 heads
-// over 8: 453 us, all on tcgen05 1334; a launch with nothing left to do costs 6.
+// tile of the other kernel stays with one SM.  This kernel runs after the other one.  512 new tokens of 4000 next
+// to 31 single ones of 32000, 64 heads over 8: 461 us, all on tcgen05 1334; a launch with nothing left to do costs 6.
 int split_rows_of(const Kv8Args& a) {
   const int group = a.n_heads / a.n_kv;
   if (attn_kv8_long_seqs(a) == a.S || !attn_kv8_tc_fits(a)) return 0;
@@ -823,7 +823,7 @@ cudaError_t launch(AttnParams p, const CUtensorMap& tmK, const CUtensorMap& tmV,
   p.desc = static_cast<int4*>(workspace);
   p.slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16 * static_cast<size_t>(blocks));
   p.warp_slots = p.slots + static_cast<size_t>(blocks) * 2 * Cfg::kSlotFloats;
-  // Where no sequence can have many steps, items are padded to a block's warps, so that none is shared between
+  // Where no sequence can have many steps (by the page table's width: the host does not know the lengths), items are padded to a block's warps, so that none is shared between
   // blocks and the second kernel need not be launched.  The padding costs balance: with up to 8 steps a
   // sequence always (a warp then takes one or two steps, or whole items where there are many), with up to 8
   // steps a warp only where every item has a block of its own.

@@ -648,12 +648,14 @@ int64_t attn_kv8_long_seqs(const Kv8Args& a) {
   return std::min<int64_t>(a.S, (a.T - a.S + a.max_new - 2) / (a.max_new - 1));
 }
 
-// Whether a call runs faster on the kernel above.  It takes 106 us for a wave of CTAs (256 rows of one sequence
+// Whether a call runs faster on the kernel above.  It takes 104 us for a wave of CTAs (256 rows of one sequence
 // and head, or what is left of them: half a CTA a sequence on average) over 4000 keys; the other kernel, which splits
-// the keys over the GPU, 37 us and 1.65 us for every tile of 128 rows.  Both grow alike with the keys.
-// Measured, 64 heads over 8, one sequence of 4000: 64 new tokens 105 against 91 us, 100: 107 against 124, 256: 106
-// against 249; 16 sequences of 33 new tokens, 32 heads over 4: 106 against 271.
-// Short sequences next to long ones run on the other kernel beside this one.
+// the keys over the GPU, 37 us and 1.65 us for every tile of 128 rows.  The host does not know the lengths, so the rule
+// takes both to grow alike with the keys; where they do not, the choice is the one for 4000.
+// Measured (here against there), 64 heads over 8, one sequence of 4000: 64 new tokens 105 against 95 us, 100: 104
+// against 124, 256: 102 against 249; 16 sequences of 33 new tokens, 32 heads over 4: 114 against 271.  This kernel
+// with 100 new tokens of 1000: 37 us, of 30000: 660.  The other with 64 of 1000: 37, of 30000: 486.
+// Short sequences next to long ones run on the other kernel, after this one.
 bool attn_kv8_tc_fits(const Kv8Args& a) {
   const int64_t group = a.n_heads / a.n_kv;
   if (a.head_dim != kD || a.S > 65535 || a.n_kv > 65535 || a.max_new * group < kBlk) return false;

@@ -18,7 +18,7 @@
 //
 // One block owns (sequence, page, a range of key/value heads): it alone writes the
 // page's codes and scale of those heads, so there are no atomics and the result does
-// not depend on timing.  The kernel is bound by memory (read 2 B, write 2 B a query
+// not depend on timing.  The bytes are the floor (read 2 B, write 2 B a query
 // element, read 2 B, write 1 B a key or value element).  A thread owns 16 elements of one
 // token for all the block's heads, so its 8 cosines and sines are computed once (in shared memory,
 // at an address of its own: 16 registers more would spill), a page's tokens are all there at once, and keys and values share one barrier a head.
@@ -26,7 +26,9 @@
 //    registers, idle threads take query heads.
 //  * More: a head's tokens come as TMA boxes through a ring in shared memory, so
 //    that loads stay in flight across the barrier: 8 prompts of 2048 tokens, 32 + 32 heads of 128, 162 us
-//    (671 MB, 4.1 TB/s, 63 % of a copy's rate; 74 M instructions at 1.7 a cycle); in registers 210 us.
+//    (671 MB, 4.1 TB/s, 63 % of a copy's rate); in registers 210 us.  Latency bounds it: 1.7 instructions a cycle
+//    of 4, a quarter of the SM's warps (one block of 512 threads), which wait for loads first; a block's angles
+//    and first boxes overlap with nothing.
 #include <cuda_fp8.h>
 
 #include "ar_internal.h"

@@ -24,7 +24,7 @@
 // of bf16), the 4 lanes of a block combine maxima and sums with two shuffles, and
 // every load of a thread's two chunks is issued before the first is used.
 // Measured: 8192 x 28672 with V and alpha given, W_hat, codes and scales written (8.66
-// bytes a weight): 304 us, 6.7 TB/s; the gradient of 4096 x 4096 (14.25 bytes): 39 us,
+// bytes a weight): 321 us, 6.3 TB/s; the gradient of 4096 x 4096 (14.25 bytes): 39 us,
 // 6.1 TB/s.  A copy of a large tensor runs at 6.4 TB/s on the same GPU.
 #include "ar_internal.h"
 

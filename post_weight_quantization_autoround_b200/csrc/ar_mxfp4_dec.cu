@@ -23,8 +23,9 @@
 //    memory.  Parts are added in a fixed order.
 //
 // 5 tokens through 8192 x 28672 (125 MB of codes and scales): 46 us, 2.7 TB/s, 42 % of a copy's
-// rate; 58 % of the issue slots and 54 % of the integer pipe are busy, about 56 instructions a
-// block and tile, half of them the box's control; 1 us of it looks for sums that are not finite.  One token 39 us (34 of them the same loop).
+// rate; 58 % of the issue slots and 55 % of the integer pipe are busy, about 58 instructions a
+// block and tile, half of them the box's control; 1 us of it looks for sums that are not finite.  One token 41 us.
+// Spans summed again take about four times as long: one in 112 2 us more, all of them 160 us.
 // Four CTAs to a cluster instead of two 48 us (132 of 148 SMs hold clusters of four), 8 warps 66 us.
 #include "ar_internal.h"
 

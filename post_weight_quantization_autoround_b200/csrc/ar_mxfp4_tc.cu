@@ -19,8 +19,8 @@
 //    TMA (128-byte swizzle).  Few tiles: the CTAs of a cluster split K and add their sums
 //    through distributed shared memory in rank order.
 //
-// 256 tokens through 8192 x 28672: 98-101 us, 1.19-1.22 PFLOP/s, tensor pipe 71 % (128 of 148 SMs have a
-// CTA); 512 tokens 176 us, 1.37 PFLOP/s; 16 tokens 86 us, where a stage's chain of expansion, hand-over and
+// 256 tokens through 8192 x 28672: 112 us in a long loop of calls, under the power cap (1.08 PFLOP/s), 98-102 for
+// single launches (1.18-1.22), tensor pipe 71 % (128 of 148 SMs have a CTA); 512 tokens 176 us, 1.37 PFLOP/s; 16 tokens 86 us, where a stage's chain of expansion, hand-over and
 // release sets the pace.  128-token tiles with the scales applied the same way: 187 us at 256 tokens.
 #include "ar_internal.h"
 
