@@ -529,7 +529,8 @@ AR_API ar_status ar_tune_step_mxfp4(const uint16_t* W, float* V, float* alpha, i
  *           to 252 (the largest ar_qdq_mxfp4 writes for finite weights) give finite
  *           weights, 255 makes the whole row NaN
  *   out     bf16 [T][N] (round to nearest even of fp32 sums), 16-byte aligned
- * Weights are exact in bf16, so only the fp32 accumulation and the output round.
+ * Weights are exact in bf16, so only the fp32 accumulation and the output round (and, at T <= 8, activations
+ * that enter in f16 by a power of two: by 2^-22 of the largest in their block of 32 at most).
  * T <= 8 decodes against the packed weights (mma.sync); larger T runs a tcgen05 GEMM
  * that expands them on the way, 256 tokens a tile; at T >= 2048 with N % 8 == 0, K <= 8192
  * and a workspace the weights are expanded once into it and the pair GEMM runs (without
